@@ -471,7 +471,9 @@ m2_status mamba2_gdn_prefill_workspace_size(const m2_pool* pool, int32_t num_seq
  * are neither read nor written.  With bf16 q, k, v and o the contractions run in
  * bf16 with fp32 accumulation; with fp32 io_dtype or o_dtype in split bf16 (three
  * products) for fp32-level accuracy.  Inputs are taken as finite: a NaN or an
- * infinity may also reach outputs up to 63 rows ahead of it in its sequence.
+ * infinity may also reach outputs up to 63 rows ahead of it in its sequence,
+ * but not past a checkpoint: the rows up to it, its state and its window are
+ * those of the rows before the NaN alone.
  * workspace: at least mamba2_gdn_prefill_workspace_size(...) bytes, 256-byte
  * aligned, scratch of this call: calls that overlap in time need one each.
  * Errors: as mamba2_prefill_chunked; M2_ERR_UNSUPPORTED as above.  On any error

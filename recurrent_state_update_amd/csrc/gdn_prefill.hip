@@ -720,7 +720,10 @@ __global__ __launch_bounds__(64 * NW) void walk_kernel(GdnPrefillParams p, int p
             float x = bias[ct];
 #pragma unroll
             for (int j = 0; j < W; ++j) x += wt[ct][j] * v[ct][r + j];
-            U[rt][ct][r] = be[r] * silu(x) - bg[r] * X[rt][ct][r];   // beta is 0 behind the chunk
+            // behind the chunk beta is 0, and the v row, perhaps one of the next chunk, is left out: it may
+            // hold a NaN, which must not reach this chunk's end state
+            const bool inside = 16 * rt + 4 * q4 + r < ce.len;
+            U[rt][ct][r] = be[r] * (inside ? silu(x) : 0.f) - bg[r] * X[rt][ct][r];
           }
       }
       // U = R + (T - I) R
@@ -1214,7 +1217,9 @@ template <int DK, int W, int WHO> __device__ __forceinline__ void conv_role(cons
       }
     }
   };
-  auto conv_rows = [&](int tau0, char* to) {
+  // SiLU(conv) of the rows held, of the chunk of `len` rows at tau0.  Rows behind the chunk, perhaps of
+  // the next one, come out as 0: they may hold a NaN, which must not reach this chunk's end state.
+  auto conv_rows = [&](int tau0, int len, char* to) {
     float x[2][W + 3];
 #pragma unroll
     for (int j = 0; j < W + 3; ++j) {
@@ -1240,7 +1245,7 @@ template <int DK, int W, int WHO> __device__ __forceinline__ void conv_role(cons
         float y = bias[ct];
 #pragma unroll
         for (int j = 0; j < W; ++j) y += wt[ct][j] * x[ct][r + j];
-        o[r] = silu(y);
+        o[r] = 16 * rt + 4 * q4 + r < len ? silu(y) : 0.f;
       }
       *reinterpret_cast<floatx4*>(to + ((ct * 4 + rt) * 64 + lane) * 16) = o;
     }
@@ -1288,8 +1293,8 @@ template <int DK, int W, int WHO> __device__ __forceinline__ void conv_role(cons
     for (int j = 0; j < W - 1; ++j)
       win[ct][j] = se.has_init ? static_cast<float>(conv[((int64_t)se.slot * p.sh.Cd + vch + ct) * (W - 1) + j]) : 0.f;
   }
-  conv_rows(0, u.smem + Ro::OFF_V);
   GdnChunk ce = chunk(0), next = ce, after = ce;
+  conv_rows(0, ce.len, u.smem + Ro::OFF_V);
   if (se.nchunk > 1) {
     next = chunk(1);
     load_rows(next.tau0, rows);
@@ -1300,7 +1305,7 @@ template <int DK, int W, int WHO> __device__ __forceinline__ void conv_role(cons
   for (int n = 0; n <= se.nchunk; ++n) {
     role_copies<DK, WHO>(p, u, n);
     if (n + 2 < se.nchunk) load_rows(after.tau0, ahead);
-    if (n + 1 < se.nchunk) conv_rows(next.tau0, u.smem + Ro::OFF_V + (n + 1) % 3 * Ro::V);
+    if (n + 1 < se.nchunk) conv_rows(next.tau0, next.len, u.smem + Ro::OFF_V + (n + 1) % 3 * Ro::V);
     if (n < se.nchunk && ce.ckpt_slot >= 0) put_window(ce.ckpt_slot, ce.tau0 + ce.len);
 #pragma unroll
     for (int j = 0; j < W + 3; ++j) rows[j] = ahead[j];

@@ -1,0 +1,46 @@
+"""GPU checks of the gated delta rule at the edges of what its calls allow: rows that are not finite, forms and sizes
+that the parity tests do not reach, views of one row.  Tolerances are those of the parity tests unless a test says
+otherwise."""
+import numpy as np
+import pytest
+import torch
+
+from tests.gpu_helpers import dev, log
+from tests.test_gpu_gdn import Layer
+
+pytestmark = pytest.mark.gpu
+
+
+def same(got, want):
+    """Bit for bit (one NaN is as good as another)."""
+    kind = torch.int16 if got.element_size() == 2 else torch.int32
+    return torch.equal(got.contiguous().view(kind), want.contiguous().view(kind))
+
+
+@pytest.mark.parametrize("shape,io", [((2, 4, 64, 48), "bf16"), ((2, 4, 64, 48), "f32"), ((1, 2, 256, 32), "bf16"),
+                                      ((1, 2, 256, 32), "f32")], ids=str)
+@pytest.mark.parametrize("what", ["q", "k", "v", "a", "b"])
+def test_rows_behind_a_checkpoint_leave_it_as_it_is(shape, io, what):
+    """A NaN or an infinity in the row right behind a checkpoint that ends a chunk early: the checkpoint's state and
+    window and the outputs up to it are those of a clean prompt, bit for bit; the next checkpoint's are not."""
+    log(f"case: gdn rows behind a checkpoint {shape} io={io} {what}")
+    T, iv = 100, 37                                   # checkpoints behind rows 36 and 73; chunks end at 37, 64, 74, 100
+    for bad in (float("nan"), float("inf")):
+        kept = []
+        for spoil in (False, True):
+            L = Layer(shape, 4, 4, 161)
+            L.seed_slots([1])
+            u, a, b = (dev(x, io) for x in L.rows(T, io))
+            q, k, v = L.pool.split_qkv(u)
+            if spoil:
+                dict(q=q, k=k, v=v, a=a, b=b)[what][iv:iv + 2] = bad
+            o = L.out(T, io)
+            L.pool.gdn_prefill(0, L.w, [0, T], [1], [1], q, k, v, a, b, o, ckpt_interval=iv, ckpt_slots=[[2, 3]])
+            torch.cuda.synchronize()
+            kept.append((o, L.pool.ssm[0, 2].clone(), L.pool.conv[0, 2].clone(), L.pool.ssm[0, 3].clone()))
+        clean, spoiled = kept
+        assert same(spoiled[0][:iv], clean[0][:iv])
+        assert same(spoiled[1], clean[1]) and same(spoiled[2], clean[2])
+        assert torch.isfinite(clean[3].float()).all()
+        if what in "kv":                              # what a row writes into the state
+            assert not torch.isfinite(spoiled[3].float()).all()
