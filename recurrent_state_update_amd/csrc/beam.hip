@@ -78,12 +78,13 @@ template <int BITS> __device__ __forceinline__ uint32_t kth_largest(uint32_t v, 
   return thr;
 }
 
-// One 16-byte piece of a row as fp32 values.
+// One 16-byte piece of a row as fp32 values, at the alignment of its elements.
 template <bool BF16> struct Piece;
 template <> struct Piece<true> {
   static constexpr int N = 8;
   static __device__ __forceinline__ void load(const void* p, int64_t i, float* o) {
-    const bf16x8 v = __builtin_nontemporal_load(reinterpret_cast<const bf16x8*>(static_cast<const bf16*>(p) + i));
+    typedef bf16 piece __attribute__((ext_vector_type(8), aligned(2)));
+    const piece v = __builtin_nontemporal_load(reinterpret_cast<const piece*>(static_cast<const bf16*>(p) + i));
 #pragma unroll
     for (int e = 0; e < 8; ++e) o[e] = static_cast<float>(v[e]);
   }
@@ -91,7 +92,8 @@ template <> struct Piece<true> {
 template <> struct Piece<false> {
   static constexpr int N = 4;
   static __device__ __forceinline__ void load(const void* p, int64_t i, float* o) {
-    const floatx4 v = __builtin_nontemporal_load(reinterpret_cast<const floatx4*>(static_cast<const float*>(p) + i));
+    typedef float piece __attribute__((ext_vector_type(4), aligned(4)));
+    const piece v = __builtin_nontemporal_load(reinterpret_cast<const piece*>(static_cast<const float*>(p) + i));
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] = v[e];
   }
@@ -119,32 +121,35 @@ template <bool BF16> __global__ __launch_bounds__(kBeamThreads) void beam_scan_k
     for (int i = tid; i < p.beams; i += kBeamThreads) ct[i] = -1;
     return;
   }
-  // The row in 16-byte pieces from its first aligned element; the up to N-1 elements on either side
-  // of the pieces are the first tile's.
+  // Piece i of the row holds its tokens i N .. i N + N-1, wherever in memory the row starts: which
+  // logits are summed together depends on their tokens alone, so that equal rows have the same sum to
+  // the last bit and their beams tie.
   const char* base = static_cast<const char*>(p.logits) + (int64_t)row * p.logits_stride * (BF16 ? 2 : 4);
-  const int es = BF16 ? 2 : 4;
-  int head = (int)((16 - (reinterpret_cast<uintptr_t>(base) & 15)) & 15) / es;
-  head = head < p.vocab ? head : p.vocab;
-  const int npiece = (p.vocab - head) / N, tail = head + npiece * N;
-  float x[PIECES][N], mx[PIECES], extra = -INFINITY;
-  int extra_tok = -1;
+  const int whole = p.vocab / N;
+  float x[PIECES][N], mx[PIECES];
+  auto piece_of = [&](int j) { return tile * (kBeamTile / N) + j * kBeamThreads + tid; };
+  auto token_of = [&](int j) { return (int)((unsigned)piece_of(j) * N); };   // the piece's first
 #pragma unroll
   for (int j = 0; j < PIECES; ++j) {
-    const int pc = tile * (kBeamTile / N) + j * kBeamThreads + tid;
-    if (pc < npiece) {
-      Piece<BF16>::load(base, (int64_t)head + (int64_t)pc * N, x[j]);
+    const int pc = piece_of(j);
+    if (pc < whole) {
+      Piece<BF16>::load(base, (int64_t)pc * N, x[j]);
     } else {
 #pragma unroll
       for (int e = 0; e < N; ++e) x[j][e] = -INFINITY;
     }
   }
-  if (tile == 0) {
-    if (tid < head) extra_tok = tid;
-    else if (tid >= 8 && tail + tid - 8 < p.vocab) extra_tok = tail + tid - 8;
-    if (extra_tok >= 0) extra = load_any(base, extra_tok, BF16);
+  if (tile == p.tiles - 1 && p.vocab % N) {   // the row's last piece, a part of one
+#pragma unroll
+    for (int j = 0; j < PIECES; ++j)
+      if (piece_of(j) == whole) {
+#pragma unroll
+        for (int e = 0; e < N - 1; ++e)
+          if (e < p.vocab % N) x[j][e] = load_any(base, (int64_t)whole * N + e, BF16);
+      }
   }
   // largest logit (NaN are passed over here and make the sum NaN)
-  float lm = extra;
+  float lm = -INFINITY;
 #pragma unroll
   for (int j = 0; j < PIECES; ++j) {
     mx[j] = x[j][0];
@@ -181,7 +186,6 @@ template <bool BF16> __global__ __launch_bounds__(kBeamThreads) void beam_scan_k
     for (int e = 0; e < N; ++e) part += term(x[j][e]);
     sum += part;
   }
-  if (extra_tok >= 0) sum += term(extra);
   const double ws = wave_sum(m > -INFINITY ? (double)sum + (double)ones : sum == sum ? 0.0 : (double)sum);
   if (lane == 0) s_sum[wave] = ws;
   // logits that reach the threshold
@@ -195,12 +199,11 @@ template <bool BF16> __global__ __launch_bounds__(kBeamThreads) void beam_scan_k
 #pragma unroll
   for (int j = 0; j < PIECES; ++j) {
     if (mx[j] > -INFINITY && ordered(mx[j]) >= thr) {
-      const int t0 = head + (tile * (kBeamTile / N) + j * kBeamThreads + tid) * N;
+      const int t0 = token_of(j);
 #pragma unroll
       for (int e = 0; e < N; ++e) offer(x[j][e], t0 + e);
     }
   }
-  if (extra_tok >= 0) offer(extra, extra_tok);
   __syncthreads();
   if (tid == 0) {
     double t = 0.0;
@@ -234,11 +237,10 @@ template <bool BF16> __global__ __launch_bounds__(kBeamThreads) void beam_scan_k
     };
 #pragma unroll
     for (int j = 0; j < PIECES; ++j) {
-      const int t0 = head + (tile * (kBeamTile / N) + j * kBeamThreads + tid) * N;
+      const int t0 = token_of(j);
 #pragma unroll
       for (int e = 0; e < N; ++e) look(x[j][e], t0 + e);
     }
-    if (extra_tok >= 0) look(extra, extra_tok);
 #pragma unroll
     for (int o = 32; o; o >>= 1) {
       const uint64_t up = __shfl_xor(best, o);
