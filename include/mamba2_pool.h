@@ -490,9 +490,12 @@ m2_status mamba2_gdn_prefill(m2_pool* pool, int32_t layer, const m2_layer_params
 /* ---- Beam search over a pool of any family: one step from logits to new beams,
  * with the states moved to where the new beams live.  Candidate (beam b, token t)
  * of a request has the score
- *   scores[b] + logits[b][t] - log sum_t' exp(logits[b][t'])      (in fp64)
+ *   scores[b] + logits[b][t] - log sum_t' exp(logits[b][t'])
  * and the request's `beams` best candidates are its new beams, best first; equal
- * scores go to the lowest b*vocab + t.  A finished beam has one candidate,
+ * scores go to the lowest b*vocab + t.  Scores are compared in fp64.  The
+ * exponentials of the sum are fp32: they put a beam's log-sum-exp off by about
+ * 1e-8, 2e-6 at most, so candidates of different beams that are nearer than that
+ * may come in either order; beams with equal rows have equal sums.  A finished beam has one candidate,
  * (b, eos_token) at scores[b].  A logit of -inf is never taken; a beam whose score
  * is not finite, or whose logits hold a NaN or +inf, has no candidate.
  *   logits    device [batch*beams][vocab] of logits_dtype, rows logits_stride apart
