@@ -342,8 +342,8 @@ class Pool:
             p, stride = _rows(t, name)
             if t.shape[1] != width or (t.shape[0] != rows if exact else t.shape[0] < rows):
                 raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {rows} rows of {width}")
-            # the stride of a single row is never used; torch gives it any value
-            args += [p, max(stride, width) if rows <= 1 else stride]
+            # the stride of a single row is never used, and a view of one row may have any
+            args += [p, width if rows <= 1 else stride]
         for t, name, shape in ((w.A, "A", (self.nheads,)), (w.dt_bias, "dt_bias", (self.nheads,)),
                                (w.conv_w, "conv_w", (self.conv_dim, self.conv_kernel)),
                                (w.conv_b, "conv_b", (self.conv_dim,))):

@@ -1,0 +1,35 @@
+"""CPU checks of what the binding of the gated delta rule makes of its arguments."""
+import numpy as np
+import pytest
+import torch
+
+from recurrent_state_update_amd.pool import LayerWeights, Pool
+
+
+@pytest.fixture
+def layer():
+    pool = Pool.allocate_gdn(1, 3, 3, 16, 32, 1, 4, device="cpu")
+    cd = pool.conv_dim
+    return pool, LayerWeights(-torch.ones(3), None, torch.zeros(3), torch.zeros(cd, 4), None)
+
+
+def strides(pool, w, rows, u, a, b, o, exact=True):
+    args = pool._gdn_rows(w, rows, *pool.split_qkv(u), a, b, o, exact)
+    return args[1:10:2] + [args[12]]          # q, k, v, a, b and o
+
+
+@pytest.mark.parametrize("rows", [0, 1])
+def test_the_stride_of_a_single_row_is_its_width(layer, rows):
+    """Whatever torch says it is: a view of a wider row, or of an expanded one."""
+    pool, w = layer
+    wide = torch.zeros(1, pool.conv_dim + 7)
+    u, a, b, o = wide[:rows, :-7], wide[:rows, -7:-4], wide[:rows, -4:-1], wide[:rows, :48]
+    assert strides(pool, w, rows, u, a, b, o) == [32, 32, 48, 3, 3, 48]
+    assert strides(pool, w, rows, u.as_strided(u.shape, (0, 1)), a, b, o) == [32, 32, 48, 3, 3, 48]
+
+
+def test_the_stride_of_several_rows_is_passed_on(layer):
+    pool, w = layer
+    wide = torch.zeros(2, pool.conv_dim + 7)
+    n = wide.shape[1]
+    assert strides(pool, w, 2, wide[:, :-7], wide[:, -7:-4], wide[:, -4:-1], wide[:, :48]) == [n] * 6

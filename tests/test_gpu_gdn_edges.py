@@ -44,3 +44,32 @@ def test_rows_behind_a_checkpoint_leave_it_as_it_is(shape, io, what):
         assert torch.isfinite(clean[3].float()).all()
         if what in "kv":                              # what a row writes into the state
             assert not torch.isfinite(spoiled[3].float()).all()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_a_single_row_may_have_any_pitch(io):
+    """One row of a projection [q | k | v | a | b] whose pitch is no multiple of 16 bytes: its stride is never used."""
+    log(f"case: gdn single row of an odd pitch io={io}")
+    shape = (1, 3, 32, 16)
+    for call in ("decode", "multi", "prefill"):
+        kept = []
+        for packed in (False, True):
+            L = Layer(shape, 4, 4, 171)
+            L.seed_slots([1])
+            u, a, b = (dev(x, io) for x in L.rows(1, io))
+            if packed:
+                wide = torch.cat([u, a, b], dim=1)                       # cd + 6 values
+                assert wide.stride(0) * wide.element_size() % 16 != 0 and wide.data_ptr() % 16 == 0
+                u, a, b = wide[:, :L.cd], wide[:, L.cd:L.cd + 3], wide[:, L.cd + 3:]
+            q, k, v = L.pool.split_qkv(u)
+            o = L.out(1, io)
+            slot = torch.tensor([1], dtype=torch.int32, device="cuda")
+            if call == "decode":
+                L.pool.gdn_decode_step(0, L.w, slot, q, k, v, a, b, o)
+            elif call == "multi":
+                L.pool.gdn_decode_multi(0, L.w, slot, slot.view(1, 1) + 1, q, k, v, a, b, o)
+            else:
+                L.pool.gdn_prefill(0, L.w, [0, 1], [1], [1], q, k, v, a, b, o)
+            torch.cuda.synchronize()
+            kept.append((o, L.pool.ssm.clone(), L.pool.conv.clone()))
+        assert all(same(x, y) for x, y in zip(*kept)), call
