@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+from recurrent_state_update_amd.pool import Pool
 from tests.gpu_helpers import log
 from tests.test_gpu_beam import draw, make_pool, run
 
@@ -50,3 +51,72 @@ def test_log_sum_exp_of_usual_rows():
     err = (out.double() - (scores.double() + (top - lse))).abs().max().item()
     log(f"  log-sum-exp off by {err:.1e}")
     assert err <= 2e-8
+
+
+@pytest.mark.parametrize("dt", DTYPES, ids=str)
+@pytest.mark.parametrize("B,K,V", [(1, 32, 40001), (2, 32, 131072), (1, 20, 100003), (1, 32, 32768)])
+def test_more_candidates_than_are_held(B, K, V, dt):
+    """ceil(V / 8192) K^2 candidates of a request: above 4096 their scores are worked out twice."""
+    log(f"case: beam candidates {B}x{K} vocab {V} {dt}")
+    _, logits, scores, slots = draw(400 + K + V, B, K, V, dt)
+    run(logits, scores, slots)
+    fin = np.zeros((B, K), np.uint8)
+    fin[:, 1::3] = 1
+    run(logits, scores, slots, finished=fin, eos=V - 1, in_place=True)
+
+
+@pytest.mark.parametrize("V", [9000, 32768, 40001], ids=lambda v: f"V{v}")
+def test_more_ties_than_the_list_holds(V):
+    """Constant rows and equal scores: all candidates tie (2048, 4096 and 5120 of them, held or not)."""
+    log(f"case: beam ties of all candidates V={V}")
+    K = 32
+    for dt in DTYPES:
+        logits, scores = torch.zeros((2, K, V), dtype=dt, device="cuda"), np.full((2, K), -1.25)
+        logits[1] = 7.0
+        slots = np.arange(2 * K).reshape(2, K)
+        run(logits, scores, slots)
+        scores[:, :5] = -9.0                          # the lowest beams are not the best
+        logits[:, 7] = -torch.inf                     # nor has every beam a candidate
+        run(logits, scores, slots, finished=(np.arange(2 * K).reshape(2, K) == 9).astype(np.uint8), eos=3)
+
+
+@pytest.mark.parametrize("V", [9000, 40001], ids=lambda v: f"V{v}")
+def test_ties_of_several_scores_within_the_threshold(V):
+    """Over 1024 candidates whose scores share their upper 32 bits but are not all equal: beam 20 has three tokens a
+    little above the ties of beams 2 and up, which come next, the lowest first; beams 0 and 1 lie a little below."""
+    log(f"case: beam nearly equal candidates V={V}")
+    K, dt = 32, torch.float32
+    logits = torch.zeros((1, K, V), dtype=dt, device="cuda")
+    scores = np.full((1, K), np.float32(-1.25), np.float32)
+    scores[0, :2] = np.nextafter(np.float32(-1.25), np.float32(-2))
+    logits[0, 20] = -torch.inf
+    logits[0, 20, [5, V // 2, V - 1]] = 3.0
+    tie = np.float64(scores[0, 2]) - np.log(V)
+    upper = lambda v: int(np.float64(v).view(np.uint64)) >> 32
+    s = np.float32(tie + np.log(3.0))
+    while np.float64(s) - np.log(3.0) <= tie:
+        s = np.nextafter(s, np.float32(0))
+    scores[0, 20] = s
+    assert upper(np.float64(s) - np.log(3.0)) == upper(tie) == upper(np.float64(scores[0, 0]) - np.log(V))
+    tok, par = run(logits, scores, np.arange(K).reshape(1, K))
+    assert par.tolist() == [20] * 3 + [2] * (K - 3) and tok.tolist() == [5, V // 2, V - 1] + list(range(K - 3))
+
+
+@pytest.mark.parametrize("family", ["mamba2 f32", "mamba2 bf16", "mamba1", "kda"])
+def test_pools_of_every_family(family):
+    """Selection and copies on the other families' pools, on a stream of its own."""
+    log(f"case: beam pool {family}")
+    f32, bf16 = torch.float32, torch.bfloat16
+    pool = {"mamba2 f32": lambda: Pool.allocate(3, 14, 4, 16, 32, 2, 4, f32, f32),
+            "mamba2 bf16": lambda: Pool.allocate(1, 14, 4, 16, 32, 2, 4, bf16, bf16),
+            "mamba1": lambda: Pool.allocate_mamba1(2, 14, 64, 16, 4),
+            "kda": lambda: Pool.allocate_kda(2, 14, 2, 32, 4)}[family]()
+    g = torch.Generator(device="cuda")
+    g.manual_seed(14)
+    for t in (pool.ssm, pool.conv):
+        t.copy_(torch.randn(t.shape, generator=g, device="cuda"))
+    _, logits, scores, slots = draw(500, 3, 4, 3001, f32)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        run(logits, scores, slots, pool=pool)
+        run(logits, scores, slots, pool=pool, in_place=True)
