@@ -389,7 +389,8 @@ class Pool:
     def _ckpt_table(ckpt_slots, ns: int):
         if ckpt_slots is None:
             return None, None, 0
-        ck = np.ascontiguousarray(np.asarray(ckpt_slots, dtype=np.int32).reshape(ns, -1))
+        # without sequences the table has no rows to tell its width by
+        ck = np.ascontiguousarray(np.asarray(ckpt_slots, dtype=np.int32).reshape(ns, -1 if ns else 0))
         return ck, ck.ctypes.data_as(c_void_p), ck.shape[1]
 
     def gdn_workspace_size(self, cu_seqlens, start_pos=None, ckpt_interval: int = 0, ckpt_slots=None,

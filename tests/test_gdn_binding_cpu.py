@@ -33,3 +33,18 @@ def test_the_stride_of_several_rows_is_passed_on(layer):
     wide = torch.zeros(2, pool.conv_dim + 7)
     n = wide.shape[1]
     assert strides(pool, w, 2, wide[:, :-7], wide[:, -7:-4], wide[:, -4:-1], wide[:, :48]) == [n] * 6
+
+
+def test_an_empty_batch_takes_an_empty_checkpoint_table(layer):
+    """No sequences: nothing to do, with a [0, max_ckpt] table as without one."""
+    pool, w = layer
+    none = np.zeros(0, np.int32)
+    assert pool.gdn_workspace_size([0], ckpt_interval=16) == 0
+    for table in (np.zeros((0, 3), np.int32), none, []):
+        assert pool.gdn_workspace_size([0], ckpt_interval=16, ckpt_slots=table) == 0
+        assert pool._ckpt_table(table, 0)[2] == 0
+    assert pool._ckpt_table([[1, 2], [-1, 0]], 2)[2] == 2 and pool._ckpt_table([1, 2], 2)[2] == 1
+    with pytest.raises(ValueError):
+        pool._ckpt_table([[1, 2]], 0)
+    with pytest.raises(ValueError):
+        pool._ckpt_table([1, 2, 3], 2)

@@ -73,3 +73,24 @@ def test_a_single_row_may_have_any_pitch(io):
             torch.cuda.synchronize()
             kept.append((o, L.pool.ssm.clone(), L.pool.conv.clone()))
         assert all(same(x, y) for x, y in zip(*kept)), call
+
+
+def test_calls_without_rows():
+    """No sequence, or only empty ones: taken, and nothing is touched."""
+    log("case: gdn calls without rows")
+    L = Layer((1, 3, 32, 16), 4, 4, 181)
+    L.seed_slots([1, 2])
+    u, a, b = (dev(x, "bf16") for x in L.rows(0, "bf16"))
+    q, k, v = L.pool.split_qkv(u)
+    o, none = L.out(0, "bf16"), torch.zeros(0, dtype=torch.int32, device="cuda")
+    before = L.pool.ssm.clone(), L.pool.conv.clone()
+    L.pool.gdn_decode_step(0, L.w, none, q, k, v, a, b, o, slots_host=[])
+    L.pool.gdn_decode_multi(0, L.w, none, none.view(0, 3), q, k, v, a, b, o, slots_in_host=[], slots_out_host=[])
+    L.pool.gdn_prefill(0, L.w, [0], [], [], q, k, v, a, b, o)
+    L.pool.gdn_prefill(0, L.w, [0], [], [], q, k, v, a, b, o, start_pos=[], ckpt_interval=8,
+                       ckpt_slots=np.zeros((0, 2), np.int32))
+    L.pool.gdn_prefill(0, L.w, [0, 0, 0], [1, 2], [1, 0], q, k, v, a, b, o, ckpt_interval=8, ckpt_slots=[[3], [-1]])
+    f = torch.zeros(0, device="cuda")
+    L.pool.beam_step(torch.zeros((0, 4, 50), device="cuda"), f, none, none, none, f, none)
+    torch.cuda.synchronize()
+    assert same(L.pool.ssm, before[0]) and same(L.pool.conv, before[1])
