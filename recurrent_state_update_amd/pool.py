@@ -17,10 +17,14 @@ from ._ffi import M2_BF16, M2_F32, Int8StoreDesc, LayerParams, Mamba2Error, Pool
 _DT = {torch.float32: M2_F32, torch.bfloat16: M2_BF16}
 
 
+def _code_of(dtype: torch.dtype) -> int:
+    if dtype not in _DT:
+        raise TypeError(f"unsupported dtype {dtype}; use float32 or bfloat16")
+    return _DT[dtype]
+
+
 def _dtype_code(t: torch.Tensor) -> int:
-    if t.dtype not in _DT:
-        raise TypeError(f"unsupported dtype {t.dtype}; use float32 or bfloat16")
-    return _DT[t.dtype]
+    return _code_of(t.dtype)
 
 
 def _rows(t: torch.Tensor, name: str):
@@ -404,7 +408,7 @@ class Pool:
         ck, ck_p, max_ck = self._ckpt_table(ckpt_slots, ns)
         n = c_uint64()
         check(lib().mamba2_gdn_prefill_workspace_size(self._h, ns, cu_p, sp_p, ckpt_interval, ck_p, max_ck,
-                                                      _DT[io_dtype], _DT[o_dtype], byref(n)))
+                                                      _code_of(io_dtype), _code_of(o_dtype), byref(n)))
         return n.value
 
     def gdn_prefill(self, layer: int, w: LayerWeights, cu_seqlens, slots, has_init, q, k, v, a, b, o, start_pos=None,

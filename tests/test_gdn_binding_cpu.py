@@ -48,3 +48,12 @@ def test_an_empty_batch_takes_an_empty_checkpoint_table(layer):
         pool._ckpt_table([[1, 2]], 0)
     with pytest.raises(ValueError):
         pool._ckpt_table([1, 2, 3], 2)
+
+
+def test_the_workspace_query_names_a_type_it_does_not_take(layer):
+    pool, _ = layer
+    for dt in (torch.float16, torch.int32):
+        with pytest.raises(TypeError, match="unsupported dtype"):
+            pool.gdn_workspace_size([0, 5], io_dtype=dt)
+        with pytest.raises(TypeError, match="unsupported dtype"):
+            pool.gdn_workspace_size([0, 5], o_dtype=dt)
