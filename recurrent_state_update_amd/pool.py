@@ -28,7 +28,8 @@ def _dtype_code(t: torch.Tensor) -> int:
 
 
 def _rows(t: torch.Tensor, name: str):
-    if t.dim() != 2 or t.stride(1) != 1:
+    # the stride of a dimension of one element, and every stride of an empty tensor, may be anything
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1 and t.numel() > 0):
         raise ValueError(f"{name} must be a 2-D tensor with a contiguous last dimension")
     return c_void_p(t.data_ptr()), t.stride(0)
 
@@ -448,8 +449,8 @@ class Pool:
         request into tokens, parents, scores_out and slots_out ([batch*beams] each, best first), and the
         states of every layer where the new beams live.  finished / finished_out are uint8; an output may
         be the input of its kind."""
-        if logits.dim() != 3 or logits.stride(2) != 1 or (min(logits.shape[:2]) > 1 and
-                                                          logits.stride(0) != logits.shape[1] * logits.stride(1)):
+        if logits.dim() != 3 or (logits.stride(2) != 1 and logits.shape[2] > 1 and logits.numel() > 0) or (
+                min(logits.shape[:2]) > 1 and logits.stride(0) != logits.shape[1] * logits.stride(1)):
             raise ValueError("logits must be [batch, beams, vocab] with evenly spaced rows and a contiguous last dimension")
         batch, beams, vocab = logits.shape
         dev, n = self.ssm.device, batch * beams
@@ -474,7 +475,7 @@ class Pool:
         elif workspace.device != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the pool's device")
         # the stride of a single row is never used; torch gives it any value
-        stride = logits.stride(1) if beams > 1 else logits.stride(0) if batch > 1 else vocab
+        stride = vocab if n <= 1 else logits.stride(1) if beams > 1 else logits.stride(0)
         with torch.cuda.device(dev):
             check(lib().mamba2_beam_step(self._h, batch, beams, vocab, c_void_p(logits.data_ptr()), stride,
                                          _dtype_code(logits), ptrs[0], ptrs[1], eos_token, ptrs[2], host_p, *ptrs[3:6],

@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from recurrent_state_update_amd.pool import LayerWeights, Pool
+from recurrent_state_update_amd.pool import LayerWeights, Pool, _rows
 
 
 @pytest.fixture
@@ -57,3 +57,13 @@ def test_the_workspace_query_names_a_type_it_does_not_take(layer):
             pool.gdn_workspace_size([0, 5], io_dtype=dt)
         with pytest.raises(TypeError, match="unsupported dtype"):
             pool.gdn_workspace_size([0, 5], o_dtype=dt)
+
+
+def test_strides_that_no_element_uses_are_not_looked_at():
+    """A dimension of one element, or an empty tensor, may have any stride; others are refused."""
+    assert _rows(torch.zeros(1, 6).t(), "a")[1] == 1                  # [6, 1]: one gate per row
+    assert _rows(torch.zeros(8).as_strided((0, 4), (0, 0)), "q")[1] == 0
+    assert _rows(torch.from_numpy(np.zeros((0, 5))), "q")
+    for bad in (torch.zeros(4, 6).t(), torch.zeros(2, 3, 4), torch.zeros(4), torch.zeros(4, 6)[:, ::2]):
+        with pytest.raises(ValueError):
+            _rows(bad, "q")

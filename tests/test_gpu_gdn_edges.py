@@ -94,3 +94,23 @@ def test_calls_without_rows():
     L.pool.beam_step(torch.zeros((0, 4, 50), device="cuda"), f, none, none, none, f, none)
     torch.cuda.synchronize()
     assert same(L.pool.ssm, before[0]) and same(L.pool.conv, before[1])
+
+
+def test_gates_of_one_head_may_be_a_transposed_row():
+    """[rows, 1] gates out of a [1, rows] tensor: the rows lie one element apart."""
+    log("case: gdn transposed gates of one head")
+    L = Layer((1, 1, 32, 16), 4, 8, 191)
+    L.seed_slots(range(5))
+    u, a, b = (dev(x, "bf16") for x in L.rows(5, "bf16"))
+    q, k, v = L.pool.split_qkv(u)
+    slots = torch.arange(5, dtype=torch.int32, device="cuda")
+    start = L.pool.ssm.clone(), L.pool.conv.clone()
+    kept = []
+    for x, y in ((a, b), (a.t().contiguous().t(), b.t().contiguous().t())):
+        L.pool.ssm.copy_(start[0]), L.pool.conv.copy_(start[1])
+        o, op = L.out(5, "bf16"), L.out(5, "bf16")
+        L.pool.gdn_decode_step(0, L.w, slots, q, k, v, x, y, o)
+        L.pool.gdn_prefill(0, L.w, [0, 5], [7], [0], q, k, v, x, y, op)
+        torch.cuda.synchronize()
+        kept.append((o, op, L.pool.ssm.clone()))
+    assert all(same(x, y) for x, y in zip(*kept))
