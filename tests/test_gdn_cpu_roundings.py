@@ -1,0 +1,40 @@
+"""CPU checks of the rounded chunk form that the GPU prefill's error is held against."""
+import numpy as np
+import pytest
+
+from oracle import gdn as orc
+from oracle.mamba2 import round_to
+from recurrent_state_update_amd import synth
+from tests import gdn_roundings
+
+
+def case(shape, T):
+    rng = np.random.default_rng(1)
+    Hk, Hv, dk, dv = shape
+    cd = 2 * Hk * dk + Hv * dv
+    ex = lambda v, t="f32": synth.cast_exact(v, t).astype(np.float64)
+    params = dict(A=ex(-np.exp(rng.uniform(0, np.log(16), Hv))), dt_bias=ex(rng.uniform(-4, -2, Hv)),
+                  conv_w=ex(rng.uniform(-0.5, 0.5, (cd, 4))), conv_b=ex(rng.uniform(-0.5, 0.5, cd)))
+    rows = [ex(rng.normal(0, 1, (T, n)), "bf16") for n in (cd, Hv, Hv)]
+    ssm = np.zeros((1, Hv, dv, dk))
+    ref = orc.prefill(shape, ssm, np.zeros((1, cd, 3)), params, np.array([0, T]), [0], [0], None, *rows)
+    return params, rows, ref, ssm[0]
+
+
+def test_without_roundings_it_is_the_recurrence(monkeypatch):
+    shape = (1, 2, 32, 16)
+    params, rows, ref, state = case(shape, 150)
+    monkeypatch.setattr(gdn_roundings, "round_to", lambda x, _: x.copy())
+    o, S = gdn_roundings.prefill(shape, params, *rows)
+    assert np.allclose(o, ref, rtol=0, atol=1e-12 * np.abs(ref).max())
+    assert np.array_equal(round_to(S, "bf16"), state) or gdn_roundings.norm_of_error(S, state) <= 2.0 ** -8
+
+
+@pytest.mark.parametrize("shape", [(2, 4, 128, 64), (2, 4, 64, 48), (1, 2, 256, 48)], ids=str)
+def test_one_plane_where_two_are_meant_shows(shape):
+    """What 5% above the two-plane form's error lets through: not one plane for T, A, U and e^(G-g) U."""
+    params, rows, ref, state = case(shape, 500)
+    two, one = (gdn_roundings.prefill(shape, params, *rows, two=n) for n in (2, 1))
+    for i, want in ((0, ref), (1, state)):
+        e2, e1 = (gdn_roundings.norm_of_error(round_to(x[i], "bf16"), want) for x in (two, one))
+        assert 1.7e-3 < e2 < 3.5e-3 and e1 > 1.1 * e2, (i, e1, e2)

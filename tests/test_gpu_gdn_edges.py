@@ -5,8 +5,12 @@ import numpy as np
 import pytest
 import torch
 
-from tests.gpu_helpers import dev, log
-from tests.test_gpu_gdn import Layer
+from oracle import gdn as orc
+from oracle.mamba2 import round_to
+from recurrent_state_update_amd.pool import Pool
+from tests import gdn_roundings
+from tests.gpu_helpers import dev, host, log
+from tests.test_gpu_gdn import LENS, SHAPES, Layer, near, run_prefill
 
 pytestmark = pytest.mark.gpu
 
@@ -114,3 +118,128 @@ def test_gates_of_one_head_may_be_a_transposed_row():
         torch.cuda.synchronize()
         kept.append((o, op, L.pool.ssm.clone()))
     assert all(same(x, y) for x, y in zip(*kept))
+
+
+def multi_against_single_steps(shape, W, K, io, odt):
+    """K tokens of three rows (one is padding, one snapshot dropped, one row ends in its own slot) and the same tokens as
+    single steps on a copy of the pool: outputs, states and windows bit for bit; the first tokens against the oracle."""
+    n = 3
+    L = Layer(shape, W, 40, 191)
+    L.seed_slots([5, 9])
+    slots_in = np.array([5, -1, 9], np.int32)
+    out = (10 + np.arange(n * K, dtype=np.int32)).reshape(n, K)
+    out[0, K - 1], out[2, 0] = 5, -1
+    rows = L.rows(n * K, io)
+    u, a, b = (dev(x, io) for x in rows)
+    q, k, v = L.pool.split_qkv(u)
+    single = Pool(L.pool.ssm.clone(), L.pool.conv.clone(), shape[1], shape[3], shape[2], shape[0], W, family=2)
+    want_s, want_c = L.pool.ssm.clone(), L.pool.conv.clone()
+    o, o1 = L.out(n * K, odt), L.out(n * K, odt)
+    sl = torch.from_numpy(slots_in).cuda()
+    L.pool.gdn_decode_multi(0, L.w, sl, torch.from_numpy(out).cuda(), q, k, v, a, b, o)
+    for t in range(K):
+        pick = torch.arange(n, device="cuda") * K + t
+        ot = L.out(n, odt)
+        single.gdn_decode_step(0, L.w, sl, q[pick], k[pick], v[pick], a[pick], b[pick], ot)
+        o1[pick] = ot
+        for i in (0, 2):
+            if out[i, t] >= 0:
+                want_s[0, out[i, t]], want_c[0, out[i, t]] = single.ssm[0, slots_in[i]], single.conv[0, slots_in[i]]
+    torch.cuda.synchronize()
+    assert same(o, o1) and same(L.pool.ssm, want_s) and same(L.pool.conv, want_c)
+    ref = orc.decode_multi(shape, L.ssm, L.conv, L.params, slots_in, out, *rows)
+    near(host(o)[0::K], ref[0::K], odt, "first tokens")
+    assert np.array_equal(host(L.pool.conv[0, out[0].tolist()]), L.conv[out[0]])
+
+
+@pytest.mark.parametrize("io,odt", [("f32", "f32"), ("bf16", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_decode_multi_of_other_types(shape, io, odt):
+    """fp32 rows enter the window rounded to bf16, for the next token of the same call too."""
+    log(f"case: gdn multi decode {shape} io={io} o={odt}")
+    multi_against_single_steps(shape, 4, 4, io, odt)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("W", [2, 3])
+def test_decode_multi_conv_widths(W, io):
+    log(f"case: gdn multi decode W={W} io={io}")
+    multi_against_single_steps((1, 3, 64, 16), W, 5, io, io)
+
+
+@pytest.mark.parametrize("lens", LENS, ids=str)
+@pytest.mark.parametrize("shape", SHAPES[:4], ids=str)
+def test_prefill_fp32_rows_bf16_output(shape, lens):
+    """fp32 rows: a bf16 output is the fp32 one rounded, bit for bit, and the slots are the same."""
+    log(f"case: gdn prefill {shape} lens={lens} io=f32 o=bf16")
+    n, T = len(lens), sum(lens)
+    L = Layer(shape, 4, 2 * n + 3, 31)
+    L.seed_slots(range(n))
+    u, a, b = (dev(x, "f32") for x in L.rows(T, "f32"))
+    q, k, v = L.pool.split_qkv(u)
+    start = L.pool.ssm.clone(), L.pool.conv.clone()
+    kept = []
+    for odt in ("f32", "bf16"):
+        L.pool.ssm.copy_(start[0]), L.pool.conv.copy_(start[1])
+        o = L.out(T, odt, 2)
+        L.pool.gdn_prefill(0, L.w, np.concatenate([[0], np.cumsum(lens)]), np.arange(n), np.arange(n) % 2, q, k, v, a, b, o)
+        torch.cuda.synchronize()
+        kept.append((o.bfloat16(), L.pool.ssm.clone(), L.pool.conv.clone()))
+    assert all(same(x, y) for x, y in zip(*kept))
+    assert (kept[1][0][T:] == 7).all()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_prefill_wide_at_dk_256(io):
+    """Several chunks and parts of dv at the largest key width, with initial states and checkpoints."""
+    log(f"case: gdn prefill wide dk 256 io={io}")
+    run_prefill(Layer((2, 4, 256, 256), 4, 30, 201), [500, 77, 130], io, io, seeded=True, interval=96,
+                starts=np.array([0, 31, 95], np.int32))
+
+
+def test_decode_of_more_rows_than_one_launch_takes():
+    """70001 rows in one call (launches of 65535), in shuffled slots: as two calls of fewer, bit for bit."""
+    log("case: gdn decode 70001 rows")
+    shape, n, cut = (1, 1, 32, 16), 70001, 40000
+    L = Layer(shape, 4, n + 5, 211)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    for t in (L.pool.ssm, L.pool.conv):
+        t.copy_(0.5 * torch.randn(t.shape, generator=g, device="cuda"))
+    u = torch.randn((n, L.cd + 2), generator=g, device="cuda")
+    rows = u[:, :L.cd].bfloat16()
+    a, b = u[:, L.cd:-1].bfloat16(), u[:, -1:].bfloat16()
+    slots = torch.randperm(n + 5, generator=g, device="cuda")[:n].to(torch.int32)
+    slots[[7, 65534, 65535, 70000]] = -1
+    other = Pool(L.pool.ssm.clone(), L.pool.conv.clone(), 1, 16, 32, 1, 4, family=2)
+    got, want = L.out(n, "bf16"), L.out(n, "bf16")
+    q, k, v = L.pool.split_qkv(rows)
+    L.pool.gdn_decode_step(0, L.w, slots, q, k, v, a, b, got)
+    for r in (slice(0, cut), slice(cut, n)):
+        other.gdn_decode_step(0, L.w, slots[r].clone(), q[r], k[r], v[r], a[r], b[r], want[r])
+    torch.cuda.synchronize()
+    assert same(got, want) and same(L.pool.ssm, other.ssm) and same(L.pool.conv, other.conv)
+    assert not got[[7, 65534, 65535, 70000]].any() and got[69999].any()
+
+
+@pytest.mark.parametrize("shape", [(2, 4, 128, 64), (2, 4, 64, 48), (1, 2, 256, 48)], ids=str)
+def test_prefill_rounds_where_it_says_and_nowhere_else(shape):
+    """bf16 rows: the 2-norm error of o and of the state against that of a CPU form in fp64 with roundings at the same
+    places of the same values.  fp32 arithmetic takes a value over a rounding border now and then, which changes single
+    errors and not their size: of the n > 3000 elements each norm is one of n errors that are independent in the main, so
+    it varies by 1/sqrt(2 n) < 1.3%, and 5% is four times that.  One rounding more, such as U or the masked Q K^T in one
+    plane, adds 10% at least (tests/test_gdn_cpu_roundings.py)."""
+    log(f"case: gdn prefill roundings {shape}")
+    T = 500
+    L = Layer(shape, 4, 3, 221)
+    rows = L.rows(T, "bf16")
+    u, a, b = (dev(x, "bf16") for x in rows)
+    o = L.out(T, "bf16")
+    L.pool.gdn_prefill(0, L.w, [0, T], [1], [0], *L.pool.split_qkv(u), a, b, o)
+    torch.cuda.synchronize()
+    ref = orc.prefill(shape, L.ssm, L.conv, L.params, np.array([0, T]), [1], [0], None, *rows)
+    sim_o, sim_s = gdn_roundings.prefill(shape, L.params, *rows)
+    for what, got, sim, want in (("o", host(o), sim_o, ref), ("state", host(L.pool.ssm[0, 1]), sim_s, L.ssm[1])):
+        err, bound = (gdn_roundings.norm_of_error(x, want) for x in (got, round_to(sim, "bf16")))
+        log(f"  {what}: error {err:.3e}, of the rounded form {bound:.3e}")
+        assert err <= 1.05 * bound, what
