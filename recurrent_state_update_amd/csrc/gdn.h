@@ -35,10 +35,10 @@ struct GdnDecodeParams {
   const float* conv_b;   // may be NULL
 };
 bool gdn_supported(int dk, int dv, int W);
-// LDS of one decode workgroup for K tokens: per token the normalised q and k, the group's v, and
-// per head alpha and beta; k.q per token; the output slots.
+// LDS of one decode workgroup for K tokens: per token the normalised q and k, the group's v, per
+// head alpha and beta, and k.q.
 inline size_t gdn_decode_lds_bytes(int rep, int dv, int dk, int K) {
-  return sizeof(float) * (size_t)K * (2 * (size_t)dk + (size_t)rep * dv + 2 * (size_t)rep + 2);
+  return sizeof(float) * (size_t)K * (2 * (size_t)dk + (size_t)rep * dv + 2 * (size_t)rep + 1);
 }
 hipError_t launch_gdn_decode(const GdnDecodeParams& p, int dk, int W, int batch, bool multi, hipStream_t s);
 

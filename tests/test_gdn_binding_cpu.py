@@ -3,7 +3,9 @@ import numpy as np
 import pytest
 import torch
 
+from recurrent_state_update_amd._ffi import lib
 from recurrent_state_update_amd.pool import LayerWeights, Pool, _rows
+from tests.test_gdn_cpu import OK, UNSUP, make, multi
 
 
 @pytest.fixture
@@ -67,3 +69,12 @@ def test_strides_that_no_element_uses_are_not_looked_at():
     for bad in (torch.zeros(4, 6).t(), torch.zeros(2, 3, 4), torch.zeros(4), torch.zeros(4, 6)[:, ::2]):
         with pytest.raises(ValueError):
             _rows(bad, "q")
+
+
+@pytest.mark.parametrize("heads,code", [(42, OK), (43, UNSUP)])
+def test_drafts_up_to_the_last_byte_of_lds(heads, code):
+    """Per token 2 dk + heads (dv + 2) + 1 floats: 3 x 13653 of them are 4 bytes below 160 KiB.  (No rows: nothing runs.)"""
+    h = make(H=heads, P=320, N=64, G=1)
+    width = heads * 320
+    assert multi(h, batch=0, tokens=3, vs=width, qs=64, ks=64, os=width, as_=heads, bs=heads) == code
+    lib().mamba2_pool_destroy(h)

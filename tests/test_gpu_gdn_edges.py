@@ -167,6 +167,12 @@ def test_decode_multi_conv_widths(W, io):
     multi_against_single_steps((1, 3, 64, 16), W, 5, io, io)
 
 
+def test_decode_multi_in_all_of_lds():
+    """42 value heads of 320 on one key head of 64, 3 tokens: 163836 bytes a workgroup."""
+    log("case: gdn multi decode, all of LDS")
+    multi_against_single_steps((1, 42, 64, 320), 4, 3, "bf16", "bf16")
+
+
 @pytest.mark.parametrize("lens", LENS, ids=str)
 @pytest.mark.parametrize("shape", SHAPES[:4], ids=str)
 def test_prefill_fp32_rows_bf16_output(shape, lens):
