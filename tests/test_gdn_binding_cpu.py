@@ -71,6 +71,16 @@ def test_strides_that_no_element_uses_are_not_looked_at():
             _rows(bad, "q")
 
 
+def test_workspace_of_fp32_rows_against_bf16_rows():
+    """What the header says of it, at the ends of the shapes."""
+    ratio = []
+    for hk, hv, dk in ((1, 64, 32), (16, 32, 128), (2, 8, 32), (8, 8, 256)):
+        pool = Pool.allocate_gdn(1, 1, hv, 16, dk, hk, 4, device="cpu")
+        size = lambda dt: pool.gdn_workspace_size([0, 64 * 400], io_dtype=dt, o_dtype=dt)
+        ratio.append(size(torch.float32) / size(torch.bfloat16))
+    assert 1.4 <= min(ratio) and max(ratio) <= 2.6 and 2.0 < ratio[1] < 2.1, ratio
+
+
 @pytest.mark.parametrize("heads,code", [(42, OK), (43, UNSUP)])
 def test_drafts_up_to_the_last_byte_of_lds(heads, code):
     """Per token 2 dk + heads (dv + 2) + 1 floats: 3 x 13653 of them are 4 bytes below 160 KiB.  (No rows: nothing runs.)"""
