@@ -19,9 +19,10 @@
 //                   chain S0 -> K S0 -> U -> S1 never leaves a wave's registers.  role_walk_kernel
 //                   for bf16 rows and dk <= 128, walk_kernel otherwise (one wave does all the work
 //                   of its columns).
-// Measured at 32 value heads of 128 x 128 over 16 key heads: 8192 rows of one sequence 311 us (launch 1
-// 82 us, bound by the VALU work of the conv and the gates at three workgroups a CU; launch 2 225 us,
-// 1.7 us a chunk), 16 x 1024 rows 446 us.
+// Measured at 32 value heads of 128 x 128 over 16 key heads: 8192 rows of one sequence 303 us (launch 1
+// 82 us: 33 of them VALU issue, 2340 instructions a wave, the rest latency that three workgroups a CU do
+// not cover; it writes 218 MB, 44 of them spilled registers; launch 2 221 us, 1.7 us a chunk), 16 x 1024
+// rows 441 us.
 // Operands are bf16, one plane each, with fp32 accumulation; or, when q, k, v or o are fp32, three
 // planes whose sum is the fp32 value, and six MFMAs a product (the terms above 2^-24 of it).
 // What the diagonals of T and Q K^T carry stays fp32 throughout: U starts from the unrounded R, and
@@ -29,7 +30,7 @@
 // largest of their sums, so this takes the 2-norm error of a bf16 call from 4.2e-3 to 2.9e-3 (of
 // which 1.7e-3 is the rounding of o itself), and costs no product.
 // The masked Q K^T, U and e^(G-g) U have two planes: 2.9e-3 becomes 2.3e-3, for o as for the states,
-// within 1.4 times the rounding that no kernel can avoid; 8192 rows take 311 us instead of 272 for it.
+// within 1.4 times the rounding that no kernel can avoid; 8192 rows took 311 us instead of 272 for it.
 // T has two planes as well: where keys repeat, U holds differences of neighbouring v whose sum over
 // the chunk must telescope, and T's roundings, each repeated down a column, would add up instead
 // (one key written 150 times without decay: 2.2e-2 of the 2-norm with one plane, 6e-3 with two).
