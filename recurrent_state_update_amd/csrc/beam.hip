@@ -45,14 +45,6 @@ __device__ __forceinline__ uint64_t ordered(double v) {
 
 // Reductions over a wave, in every lane: inside 16 lanes by data-parallel primitives (quads, then the
 // mirrored half row and row), across them by two exchanges.
-template <int CTRL> __device__ __forceinline__ float dpp(float v) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
-}
-template <int CTRL> __device__ __forceinline__ double dpp(double v) {
-  const int2 w = __builtin_bit_cast(int2, v);
-  return __builtin_bit_cast(double, int2{__builtin_amdgcn_update_dpp(0, w.x, CTRL, 0xf, 0xf, true),
-                                         __builtin_amdgcn_update_dpp(0, w.y, CTRL, 0xf, 0xf, true)});
-}
 template <typename T, typename F> __device__ __forceinline__ T wave_reduce(T v, F&& f) {
   v = f(v, dpp<0xB1>(v));
   v = f(v, dpp<0x4E>(v));

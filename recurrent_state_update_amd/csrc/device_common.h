@@ -1,6 +1,6 @@
 // Device helpers shared by the gfx950 kernels: dtype conversion, 16-byte
-// vector access, the elementwise functions of the Mamba2 layer, and the
-// bf16 MFMA tile product.
+// vector access, the elementwise functions of the Mamba2 layer, exchanges
+// between lanes, and the bf16 MFMA tile product.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -58,6 +58,28 @@ __device__ __forceinline__ float softplus(float v) {
   const float u = 1.f + e;
   const float um1 = u - 1.f;
   return um1 == 0.f ? e : __builtin_amdgcn_logf(u) * 0.6931471805599453f * e * __builtin_amdgcn_rcpf(um1);
+}
+
+// ------------------------------------------------------------------ lanes
+// The value of the lane that the data-parallel control CTRL names, within 16 lanes.
+template <int CTRL> __device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+template <int CTRL> __device__ __forceinline__ double dpp(double v) {
+  const int2 w = __builtin_bit_cast(int2, v);
+  return __builtin_bit_cast(double, int2{__builtin_amdgcn_update_dpp(0, w.x, CTRL, 0xf, 0xf, true),
+                                         __builtin_amdgcn_update_dpp(0, w.y, CTRL, 0xf, 0xf, true)});
+}
+// Sum over aligned groups of LPR lanes; every lane gets the sum.  Within 16 lanes by data-parallel
+// primitives: exchanges inside quads, then the mirrored half row and row (whose quads, then
+// halves, already agree).
+template <int LPR> __device__ __forceinline__ float group_sum(float v) {
+  if constexpr (LPR >= 2) v += dpp<0xB1>(v);    // quad_perm 1,0,3,2
+  if constexpr (LPR >= 4) v += dpp<0x4E>(v);    // quad_perm 2,3,0,1
+  if constexpr (LPR >= 8) v += dpp<0x141>(v);   // row_half_mirror
+  if constexpr (LPR >= 16) v += dpp<0x140>(v);  // row_mirror
+  if constexpr (LPR >= 32) v += __shfl_xor(v, 16);
+  return v;
 }
 
 // ------------------------------------------------------------------ MFMA

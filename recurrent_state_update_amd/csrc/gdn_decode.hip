@@ -39,21 +39,6 @@ __device__ __forceinline__ int uniform_i32(const int32_t* p) {
   return *(const cint*)p;
 }
 
-template <int CTRL> __device__ __forceinline__ float dpp(float v) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
-}
-// Sum over aligned groups of LPR lanes; every lane gets the sum.  Within 16 lanes by data-parallel
-// primitives: exchanges inside quads, then the mirrored half row and row (whose quads, then
-// halves, already agree).
-template <int LPR> __device__ __forceinline__ float group_sum(float v) {
-  if constexpr (LPR >= 2) v += dpp<0xB1>(v);    // quad_perm 1,0,3,2
-  if constexpr (LPR >= 4) v += dpp<0x4E>(v);    // quad_perm 2,3,0,1
-  if constexpr (LPR >= 8) v += dpp<0x141>(v);   // row_half_mirror
-  if constexpr (LPR >= 16) v += dpp<0x140>(v);  // row_mirror
-  if constexpr (LPR >= 32) v += __shfl_xor(v, 16);
-  return v;
-}
-
 __device__ __forceinline__ float sigmoid(float v) { return __builtin_amdgcn_rcpf(1.0f + __expf(-v)); }
 
 // DK: head_k_dim.  MULTI: K tokens with a snapshot slot each; else one token in place.

@@ -56,19 +56,6 @@ struct alignas(16) PrepArgs {   // the first launch's one argument
   int32_t tab[kGdnInlineBytes / 4];
 };
 
-template <int CTRL> __device__ __forceinline__ float dpp(float v) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
-}
-// Sum over aligned groups of LPR lanes, in every lane.
-template <int LPR> __device__ __forceinline__ float group_sum(float v) {
-  if constexpr (LPR >= 2) v += dpp<0xB1>(v);
-  if constexpr (LPR >= 4) v += dpp<0x4E>(v);
-  if constexpr (LPR >= 8) v += dpp<0x141>(v);
-  if constexpr (LPR >= 16) v += dpp<0x140>(v);
-  if constexpr (LPR >= 32) v += __shfl_xor(v, 16);
-  return v;
-}
-
 typedef uint16_t u16;
 typedef u16 u16x4 __attribute__((ext_vector_type(4)));
 typedef u16 u16x8 __attribute__((ext_vector_type(8)));
