@@ -635,16 +635,7 @@ m2_status mamba2_decode_step(m2_pool* pool, int32_t layer, const m2_layer_params
   if (m2::decode_lds_bytes(sh.H / sh.G, sh.P, sh.N) > m2::kMaxLdsBytes)
     return fail(M2_ERR_UNSUPPORTED, "decode: a group of %d heads x %d rows needs more LDS per workgroup than %zu bytes",
                 sh.H / sh.G, sh.P, m2::kMaxLdsBytes);
-  if (slots_host) {
-    std::vector<uint8_t> seen(pool->d.num_slots, 0);
-    for (int i = 0; i < batch; ++i) {
-      const int s = slots_host[i];
-      if (s == -1) continue;
-      if (s < 0 || s >= pool->d.num_slots) return fail(M2_ERR_SLOT, "slot %d of row %d out of range", s, i);
-      if (seen[s]) return fail(M2_ERR_SLOT, "slot %d appears twice", s);
-      seen[s] = 1;
-    }
-  }
+  if (m2_status st = check_row_slots(pool, batch, slots_host)) return st;
   m2::DecodeParams p;
   p.ssm = static_cast<char*>(pool->d.ssm_base) + (uint64_t)layer * pool->d.num_slots * pool->ssm_slot_bytes;
   p.conv = static_cast<char*>(pool->d.conv_base) + (uint64_t)layer * pool->d.num_slots * pool->conv_slot_bytes;
@@ -727,23 +718,8 @@ m2_status mamba2_prefill_chunked(m2_pool* pool, int32_t layer, const m2_layer_pa
   if (!slots || !has_init) return fail(M2_ERR_ARG, "slots and has_initial_state are required");
   const int64_t T = cu_seqlens[num_seqs];
   const bool ckpt_on = ckpt_interval > 0 && max_ckpt > 0;
-  const int S = pool->d.num_slots;
-  std::vector<uint8_t> used(S, 0);
-  for (int s = 0; s < num_seqs; ++s) {
-    const int sl = slots[s];
-    if (sl < 0 || sl >= S) return fail(M2_ERR_SLOT, "slot %d of sequence %d out of range", sl, s);
-    if (used[sl]) return fail(M2_ERR_SLOT, "slot %d appears twice", sl);
-    used[sl] = 1;
-  }
-  if (ckpt_on) {
-    for (int64_t i = 0; i < (int64_t)num_seqs * max_ckpt; ++i) {
-      const int sl = ckpt_slots[i];
-      if (sl == -1) continue;
-      if (sl < 0 || sl >= S) return fail(M2_ERR_SLOT, "checkpoint slot %d out of range", sl);
-      if (used[sl]) return fail(M2_ERR_SLOT, "checkpoint slot %d repeats or aliases a sequence slot", sl);
-      used[sl] = 1;
-    }
-  }
+  if (m2_status st = check_prefill_slots(pool, num_seqs, slots, ckpt_slots, ckpt_on ? (int64_t)num_seqs * max_ckpt : 0))
+    return st;
   if (T == 0) return ok();
   const int ies = esize(io_dtype);
   const int GN = sh.G * sh.N;
@@ -954,28 +930,8 @@ m2_status mamba2_decode_multi(m2_pool* pool, int32_t layer, const m2_layer_param
   if (!m2::decode_supported(pool->d.ssm_dtype == M2_BF16, sh.N, sh.W))
     return fail(M2_ERR_UNSUPPORTED, "decode supports d_state in {16,32,64,128,256}, got %d", sh.N);
   if ((int64_t)batch > 65535) return fail(M2_ERR_UNSUPPORTED, "at most 65535 sequences per multi-token call");
-  if (slots_in_host && slots_out_host) {
-    const int S = pool->d.num_slots;
-    std::vector<int> in_row(S, -1);   // the row that reads each slot
-    for (int i = 0; i < batch; ++i) {
-      const int s = slots_in_host[i];
-      if (s == -1) continue;
-      if (s < 0 || s >= S) return fail(M2_ERR_SLOT, "input slot %d of row %d out of range", s, i);
-      if (in_row[s] >= 0) return fail(M2_ERR_SLOT, "input slot %d appears twice", s);
-      in_row[s] = i;
-    }
-    std::vector<uint8_t> written(S, 0);
-    for (int64_t i = 0; i < (int64_t)batch * num_tokens; ++i) {
-      const int o = slots_out_host[i];
-      if (o == -1) continue;
-      const int row = (int)(i / num_tokens);
-      if (o < 0 || o >= S) return fail(M2_ERR_SLOT, "output slot %d of row %d out of range", o, row);
-      if (written[o]) return fail(M2_ERR_SLOT, "output slot %d appears twice", o);
-      if (in_row[o] >= 0 && in_row[o] != row)
-        return fail(M2_ERR_SLOT, "output slot %d of row %d is the input slot of row %d", o, row, in_row[o]);
-      written[o] = 1;
-    }
-  }
+  if (slots_in_host && slots_out_host)
+    if (m2_status st = check_snapshot_slots(pool, batch, num_tokens, slots_in_host, slots_out_host)) return st;
   m2::MultiDecodeParams m;
   m2::DecodeParams& p = m.d;
   p.ssm = static_cast<char*>(pool->d.ssm_base) + (uint64_t)layer * pool->d.num_slots * pool->ssm_slot_bytes;
@@ -1036,16 +992,7 @@ m2_status mamba1_decode_step(m2_pool* pool, int32_t layer, const m2_layer_params
   if (m2_status st = check_io(io, 6)) return st;
   if (!m2::mamba1_supported(sh.N, sh.W))
     return fail(M2_ERR_UNSUPPORTED, "Mamba1 decode supports d_state in {8,16,32,64,128,256}, got %d", sh.N);
-  if (slots_host) {
-    std::vector<uint8_t> seen(pool->d.num_slots, 0);
-    for (int i = 0; i < batch; ++i) {
-      const int s = slots_host[i];
-      if (s == -1) continue;
-      if (s < 0 || s >= pool->d.num_slots) return fail(M2_ERR_SLOT, "slot %d of row %d out of range", s, i);
-      if (seen[s]) return fail(M2_ERR_SLOT, "slot %d appears twice", s);
-      seen[s] = 1;
-    }
-  }
+  if (m2_status st = check_row_slots(pool, batch, slots_host)) return st;
   m2::Mamba1Params p;
   p.ssm = static_cast<char*>(pool->d.ssm_base) + (uint64_t)layer * pool->d.num_slots * pool->ssm_slot_bytes;
   p.conv = static_cast<char*>(pool->d.conv_base) + (uint64_t)layer * pool->d.num_slots * pool->conv_slot_bytes;
