@@ -499,29 +499,31 @@ __device__ __forceinline__ bf16x8 tr_frag(const u16* t, int step) {
   return __builtin_bit_cast(bf16x8, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
 }
 
+constexpr int kWalkWaves = 2;   // of a walk_kernel workgroup, 16 columns of dv each
+
 // What a walk workgroup stages in LDS per chunk: K, Q, T, the masked Q K^T and the gates as they lie
 // in the workspace, and per wave the raw v rows of its columns with the W-1 rows ahead of them.  Row
 // i of those is at slot (i % 4) * 17 + i / 4: the four lane groups of an accumulator tile read rows
 // 4 apart, which so lie side by side in the banks.
-template <int DK, int NP, int NW, int CT, typename IO> struct Stage {
+template <int DK, int NP, typename IO> struct Stage {
   static constexpr int KQ = gdn_kq_bytes(DK, NP), HEAD = gdn_head_bytes(NP);
-  static constexpr int SLOTS = 68, SLOT_BYTES = 16 * CT * (int)sizeof(IO);
+  static constexpr int SLOTS = 68, SLOT_BYTES = 16 * (int)sizeof(IO);
   static constexpr int V_OPS = (SLOTS * SLOT_BYTES + 1023) / 1024;   // wave-wide copies of one wave's v
   // Q stays in global memory where all of it does not fit (dk 256 in three planes)
-  static constexpr bool Q_IN = KQ + HEAD + NW * V_OPS * 1024 <= (int)kMaxLdsBytes;
+  static constexpr bool Q_IN = KQ + HEAD + kWalkWaves * V_OPS * 1024 <= (int)kMaxLdsBytes;
   static constexpr int KIN = Q_IN ? KQ : KQ / 2;
-  static constexpr int BYTES = KIN + HEAD + NW * V_OPS * 1024;
+  static constexpr int BYTES = KIN + HEAD + kWalkWaves * V_OPS * 1024;
   static constexpr int PIECES = (KIN + HEAD) / 1024;
   static_assert(BYTES <= (int)kMaxLdsBytes, "LDS of a walk workgroup");
   static_assert(KQ % 1024 == 0 && HEAD % 1024 == 0, "whole pieces");
 };
 
-// One workgroup of NW waves per (sequence, value head, NW * CT * 16 columns of dv); lane l of a wave
-// has the columns (l % 16) * CT + 0 .. CT-1 of the wave's.  NB stages in LDS: with two, the next
-// chunk's operands travel while this one is computed.
-template <int DK, int W, int NP, int NW, int CT, int NB, typename IO>
-__global__ __launch_bounds__(64 * NW) void walk_kernel(GdnPrefillParams p, int parts, int groups) {
-  typedef Stage<DK, NP, NW, CT, IO> St;
+// One workgroup of kWalkWaves waves per (sequence, value head, 32 columns of dv); lane l of a wave has
+// the column l % 16 of the wave's 16.  NB stages in LDS: with two, the next chunk's operands travel while
+// this one is computed.
+template <int DK, int W, int NP, int NB, typename IO>
+__global__ __launch_bounds__(64 * kWalkWaves) void walk_kernel(GdnPrefillParams p, int parts, int groups) {
+  typedef Stage<DK, NP, IO> St;
   constexpr int KS = DK / 32, NT = DK / 16, NPT = gdn_t_planes(NP);
   extern __shared__ char smem[];
   const int lane = threadIdx.x & 63, q4 = lane >> 4, l16 = lane & 15;
@@ -535,46 +537,38 @@ __global__ __launch_bounds__(64 * NW) void walk_kernel(GdnPrefillParams p, int p
   const int g = grp % p.sh.Hk, h = g * rep + in / parts;
   const GdnSeq se = load_uniform<GdnSeq>((cchar*)(p.seqs + grp / p.sh.Hk));
   if (se.nchunk == 0) return;
-  const int c0 = (in % parts * NW + wave) * CT * 16;      // the wave's first column of dv
+  const int c0 = (in % parts * kWalkWaves + wave) * 16;   // the wave's first column of dv
   const bool active = c0 < dv;
   bf16* const ssm = static_cast<bf16*>(p.ssm);
   bf16* const conv = static_cast<bf16*>(p.conv);
-  int col[CT], gc[CT];
-  bool has[CT];
-  float wt[CT][W], win[CT][W - 1], bias[CT];
-  floatx4 S[NT][CT];
+  const bool has = c0 + l16 < dv;
+  const int col = has ? c0 + l16 : dv - 1;                // a lane without a column repeats the last one
+  const int gc = 2 * p.sh.Hk * DK + h * dv + col;         // its conv channel
+  float wt[W], win[W - 1];
+  floatx4 S[NT];
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct) {
-    const int cc = c0 + l16 * CT + ct;
-    has[ct] = cc < dv;
-    col[ct] = has[ct] ? cc : dv - 1;                      // a lane without a column repeats the last one
-    gc[ct] = 2 * p.sh.Hk * DK + h * dv + col[ct];         // its conv channel
+  for (int j = 0; j < W; ++j) wt[j] = p.conv_w[(int64_t)gc * W + j];
+  const float bias = p.conv_b ? p.conv_b[gc] : 0.f;
 #pragma unroll
-    for (int j = 0; j < W; ++j) wt[ct][j] = p.conv_w[(int64_t)gc[ct] * W + j];
-    bias[ct] = p.conv_b ? p.conv_b[gc[ct]] : 0.f;
+  for (int j = 0; j < W - 1; ++j)
+    win[j] = se.has_init ? static_cast<float>(conv[((int64_t)se.slot * p.sh.Cd + gc) * (W - 1) + j]) : 0.f;
+  const bf16* sp = ssm + (((int64_t)se.slot * p.sh.Hv + h) * dv + col) * DK + 4 * q4;
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j)
-      win[ct][j] = se.has_init ? static_cast<float>(conv[((int64_t)se.slot * p.sh.Cd + gc[ct]) * (W - 1) + j]) : 0.f;
-    const bf16* sp = ssm + (((int64_t)se.slot * p.sh.Hv + h) * dv + col[ct]) * DK + 4 * q4;
+  for (int i = 0; i < NT; ++i) {
+    const u16x4 x = se.has_init ? *reinterpret_cast<const u16x4*>(sp + 16 * i) : u16x4{0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const u16x4 x = se.has_init ? *reinterpret_cast<const u16x4*>(sp + 16 * i) : u16x4{0, 0, 0, 0};
-#pragma unroll
-      for (int r = 0; r < 4; ++r) S[i][ct][r] = static_cast<float>(__builtin_bit_cast(bf16, (u16)x[r]));
-    }
+    for (int r = 0; r < 4; ++r) S[i][r] = static_cast<float>(__builtin_bit_cast(bf16, (u16)x[r]));
   }
   const IO* const vbase = static_cast<const IO*>(p.v) + (int64_t)se.t0 * p.v_stride + h * dv;
 
   auto put_slot = [&](int slot, int end) {   // state and window after `end` rows of the sequence
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-      if (!has[ct]) continue;
-      bf16* sp = ssm + (((int64_t)slot * p.sh.Hv + h) * dv + col[ct]) * DK + 4 * q4;
+    if (has) {
+      bf16* sp = ssm + (((int64_t)slot * p.sh.Hv + h) * dv + col) * DK + 4 * q4;
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         u16x4 o;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) o[r] = bits(from_f32<bf16>(S[i][ct][r]));
+        for (int r = 0; r < 4; ++r) o[r] = bits(from_f32<bf16>(S[i][r]));
         *reinterpret_cast<u16x4*>(sp + 16 * i) = o;
       }
       if (q4 == 0) {
@@ -583,12 +577,12 @@ __global__ __launch_bounds__(64 * NW) void walk_kernel(GdnPrefillParams p, int p
           const int tau = end - (W - 1) + j;
           float x = 0.f;
           if (tau >= 0) {
-            x = to_f32(vbase[(int64_t)tau * p.v_stride + col[ct]]);
+            x = to_f32(vbase[(int64_t)tau * p.v_stride + col]);
           } else {
 #pragma unroll
-            for (int i = 0; i < W - 1; ++i) x = tau == i - (W - 1) ? win[ct][i] : x;
+            for (int i = 0; i < W - 1; ++i) x = tau == i - (W - 1) ? win[i] : x;
           }
-          conv[((int64_t)slot * p.sh.Cd + gc[ct]) * (W - 1) + j] = from_f32<bf16>(x);
+          conv[((int64_t)slot * p.sh.Cd + gc) * (W - 1) + j] = from_f32<bf16>(x);
         }
       }
     }
@@ -616,8 +610,8 @@ __global__ __launch_bounds__(64 * NW) void walk_kernel(GdnPrefillParams p, int p
     const char* kq = p.kq + ((int64_t)c * p.sh.Hk + g) * St::KQ;
     const char* hd = p.head + ((int64_t)c * p.sh.Hv + h) * St::HEAD;
 #pragma unroll
-    for (int i = 0; i < (St::PIECES + NW - 1) / NW; ++i) {
-      const int pc = i * NW + wave;
+    for (int i = 0; i < (St::PIECES + kWalkWaves - 1) / kWalkWaves; ++i) {
+      const int pc = i * kWalkWaves + wave;
       if (pc < St::PIECES)
         dma16((pc * 1024 < St::KIN ? kq + pc * 1024 : hd + (pc * 1024 - St::KIN)) + lane * 16, to + pc * 1024);
     }
@@ -651,18 +645,14 @@ __global__ __launch_bounds__(64 * NW) void walk_kernel(GdnPrefillParams p, int p
       const u16* const Af = Tf + gdn_t_bytes(NP) / 2;
       const float* const g1 = reinterpret_cast<const float*>(Tf + NPT * kTri) + 4 * q4;
       const float* const g2 = reinterpret_cast<const float*>(Af + NPT * kTri) + 4 * q4;
-      const IO* const vs = reinterpret_cast<const IO*>(st + St::KIN + St::HEAD + wave * St::V_OPS * 1024) + l16 * CT;
+      const IO* const vs = reinterpret_cast<const IO*>(st + St::KIN + St::HEAD + wave * St::V_OPS * 1024) + l16;
       // K S0 and Q S0
-      floatx4 X[4][CT], Y[4][CT];
+      floatx4 X[4], Y[4];
 #pragma unroll
-      for (int rt = 0; rt < 4; ++rt)
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) X[rt][ct] = Y[rt][ct] = floatx4{0.f, 0.f, 0.f, 0.f};
+      for (int rt = 0; rt < 4; ++rt) X[rt] = Y[rt] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        Op<NP> sf[CT];
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) sf[ct] = acc_op<NP>(S[2 * ks][ct], S[2 * ks + 1][ct]);
+        const Op<NP> sf = acc_op<NP>(S[2 * ks], S[2 * ks + 1]);
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
           Op<NP> k;
@@ -673,121 +663,90 @@ __global__ __launch_bounds__(64 * NW) void walk_kernel(GdnPrefillParams p, int p
             k.p[i] = __builtin_bit_cast(bf16x8, u16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
           }
           const Op<NP> q = get_op<NP>(Qf, C * DK, rt * KS + ks, lane);
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct) {
-            X[rt][ct] = mul(k, sf[ct], X[rt][ct]);
-            Y[rt][ct] = mul(q, sf[ct], Y[rt][ct]);
-          }
+          X[rt] = mul(k, sf, X[rt]);
+          Y[rt] = mul(q, sf, Y[rt]);
         }
       }
       // R = beta (V - e^g K S0)
-      floatx4 U[4][CT];
+      floatx4 U[4];
 #pragma unroll
       for (int rt = 0; rt < 4; ++rt) {
         const floatx4 be = *reinterpret_cast<const floatx4*>(g1 + 16 * rt);
         const floatx4 bg = *reinterpret_cast<const floatx4*>(g1 + C + 16 * rt);
-        float v[CT][W + 3];
+        float v[W + 3];
 #pragma unroll
         for (int j = 0; j < W + 3; ++j) {
-          const IO* vr = vs + ((j & 3) * 17 + 4 * rt + q4 + (j >> 2)) * 16 * CT;   // row 16 rt + 4 q4 + j - (W-1)
+          const IO* vr = vs + ((j & 3) * 17 + 4 * rt + q4 + (j >> 2)) * 16;   // row 16 rt + 4 q4 + j - (W-1)
           const int tau = ce.tau0 + 16 * rt + 4 * q4 + j - (W - 1);
+          float x = to_f32(*vr);
+          if (rt == 0 && j < W - 1) {                    // rows ahead of the sequence: the window
 #pragma unroll
-          for (int ct = 0; ct < CT; ++ct) {
-            float x = to_f32(vr[ct]);
-            if (rt == 0 && j < W - 1) {                    // rows ahead of the sequence: the window
-#pragma unroll
-              for (int i = 0; i < W - 1; ++i) x = tau == i - (W - 1) ? win[ct][i] : x;
-            }
-            v[ct][j] = x;
+            for (int i = 0; i < W - 1; ++i) x = tau == i - (W - 1) ? win[i] : x;
           }
+          v[j] = x;
         }
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
+        for (int r = 0; r < 4; ++r) {
+          float x = bias;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            float x = bias[ct];
-#pragma unroll
-            for (int j = 0; j < W; ++j) x += wt[ct][j] * v[ct][r + j];
-            // behind the chunk beta is 0, and the v row, perhaps one of the next chunk, is left out: it may
-            // hold a NaN, which must not reach this chunk's end state
-            const bool inside = 16 * rt + 4 * q4 + r < ce.len;
-            U[rt][ct][r] = be[r] * (inside ? silu(x) : 0.f) - bg[r] * X[rt][ct][r];
-          }
+          for (int j = 0; j < W; ++j) x += wt[j] * v[r + j];
+          // behind the chunk beta is 0, and the v row, perhaps one of the next chunk, is left out: it may
+          // hold a NaN, which must not reach this chunk's end state
+          const bool inside = 16 * rt + 4 * q4 + r < ce.len;
+          U[rt][r] = be[r] * (inside ? silu(x) : 0.f) - bg[r] * X[rt][r];
+        }
       }
       // U = R + (T - I) R
       {
-        Op<NP> rf[2][CT];
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-          rf[0][ct] = acc_op<NP>(U[0][ct], U[1][ct]);
-          rf[1][ct] = acc_op<NP>(U[2][ct], U[3][ct]);
-        }
+        const Op<NP> rf[2] = {acc_op<NP>(U[0], U[1]), acc_op<NP>(U[2], U[3])};
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
           for (int ks = 0; ks <= rt / 2; ++ks) {
             const Op<NPT> t = get_op<NPT>(Tf, kTri, gdn_tri(rt, ks), lane);
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) U[rt][ct] = mul(t, rf[ks][ct], U[rt][ct]);
+            U[rt] = mul(t, rf[ks], U[rt]);
           }
       }
       // S1 = e^G S0 + K^T (e^(G-g) U)
       {
-        Op<NPT> uf[2][CT];
-        floatx4 w[4][CT];
+        floatx4 w[4];
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
           const floatx4 eG = *reinterpret_cast<const floatx4*>(g1 + 2 * C + 16 * rt);
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct) w[rt][ct] = U[rt][ct] * eG;
+          w[rt] = U[rt] * eG;
         }
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-          uf[0][ct] = acc_op<NPT>(w[0][ct], w[1][ct]);
-          uf[1][ct] = acc_op<NPT>(w[2][ct], w[3][ct]);
-        }
+        const Op<NPT> uf[2] = {acc_op<NPT>(w[0], w[1]), acc_op<NPT>(w[2], w[3])};
         const float decay = g1[3 * C];
         const u16* const tr = Kt + ((l16 & 3) * 16 + 4 * q4 + (l16 >> 2)) * 4;
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct) S[i][ct] = S[i][ct] * decay;
+          S[i] = S[i] * decay;
 #pragma unroll
           for (int ks = 0; ks < 2; ++ks) {
             Op<NP> k;
 #pragma unroll
             for (int pl = 0; pl < NP; ++pl) k.p[pl] = tr_frag(tr + pl * C * DK + (2 * ks * NT + i) * 256, NT * 256);
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) S[i][ct] = mul(k, uf[ks][ct], S[i][ct]);
+            S[i] = mul(k, uf[ks], S[i]);
           }
         }
       }
       // O = e^g Q S0 + q.k U + (Q K^T below the diagonal) U
       {
-        Op<NPT> uf[2][CT];
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-          uf[0][ct] = acc_op<NPT>(U[0][ct], U[1][ct]);
-          uf[1][ct] = acc_op<NPT>(U[2][ct], U[3][ct]);
-        }
+        const Op<NPT> uf[2] = {acc_op<NPT>(U[0], U[1]), acc_op<NPT>(U[2], U[3])};
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
           const floatx4 eg = *reinterpret_cast<const floatx4*>(g2 + 16 * rt);
           const floatx4 qk = *reinterpret_cast<const floatx4*>(g2 + C + 16 * rt);
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct) Y[rt][ct] = eg * Y[rt][ct] + qk * U[rt][ct];
+          Y[rt] = eg * Y[rt] + qk * U[rt];
 #pragma unroll
           for (int ks = 0; ks <= rt / 2; ++ks) {
             const Op<NPT> a = get_op<NPT>(Af, kTri, gdn_tri(rt, ks), lane);
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) Y[rt][ct] = mul(a, uf[ks][ct], Y[rt][ct]);
+            Y[rt] = mul(a, uf[ks], Y[rt]);
           }
         }
       }
-#pragma unroll
-      for (int i = 0; i < NT; ++i) pin(S[i]);
-#pragma unroll
-      for (int rt = 0; rt < 4; ++rt) pin(Y[rt]);
+      pin(S);
+      pin(Y);
       settle();
 #pragma unroll
       for (int rt = 0; rt < 4; ++rt)
@@ -796,9 +755,7 @@ __global__ __launch_bounds__(64 * NW) void walk_kernel(GdnPrefillParams p, int p
           const int i = 16 * rt + 4 * q4 + r;
           if (i < ce.len) {
             const int64_t at = ((int64_t)se.t0 + ce.tau0 + i) * p.o_stride + h * dv;
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-              if (has[ct]) store_any(p.o, at + col[ct], Y[rt][ct][r], NP == 1 ? 1 : p.o_bf16);
+            if (has) store_any(p.o, at + col, Y[rt][r], NP == 1 ? 1 : p.o_bf16);
           }
         }
       if (ce.ckpt_slot >= 0) put_slot(ce.ckpt_slot, ce.tau0 + ce.len);
@@ -812,16 +769,16 @@ __global__ __launch_bounds__(64 * NW) void walk_kernel(GdnPrefillParams p, int p
   if (active) put_slot(se.slot, se.len);
 }
 
-template <int DK, int W, int NP, int NW, int CT, typename IO> hipError_t launch_walk(const GdnPrefillParams& p, hipStream_t s) {
-  typedef Stage<DK, NP, NW, CT, IO> St;
+template <int DK, int W, int NP, typename IO> hipError_t launch_walk(const GdnPrefillParams& p, hipStream_t s) {
+  typedef Stage<DK, NP, IO> St;
   constexpr int NB = 2 * St::BYTES <= (int)kMaxLdsBytes ? 2 : 1;
-  const auto f = &walk_kernel<DK, W, NP, NW, CT, NB, IO>;
+  const auto f = &walk_kernel<DK, W, NP, NB, IO>;
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(f), hipFuncAttributeMaxDynamicSharedMemorySize,
                                            NB * St::BYTES);
   if (e != hipSuccess) return e;
-  const int parts = (p.sh.dv + NW * CT * 16 - 1) / (NW * CT * 16), groups = p.num_seqs * p.sh.Hk;
+  const int parts = (p.sh.dv + kWalkWaves * 16 - 1) / (kWalkWaves * 16), groups = p.num_seqs * p.sh.Hk;
   const int grid = (groups + 7) / 8 * 8 * (p.sh.Hv / p.sh.Hk) * parts;
-  hipLaunchKernelGGL(f, dim3(grid), dim3(64 * NW), NB * St::BYTES, s, p, parts, groups);
+  hipLaunchKernelGGL(f, dim3(grid), dim3(64 * kWalkWaves), NB * St::BYTES, s, p, parts, groups);
   return hipGetLastError();
 }
 
@@ -1369,7 +1326,7 @@ template <int DK, int W, int NP, typename IO> hipError_t launch_io(const PrepArg
   if (e != hipSuccess) return e;
   // dk 256 leaves no room for the roles' stages in LDS, three planes neither
   if constexpr (NP == 1 && DK <= 128) return launch_role_walk<DK, W>(a.p, s);
-  else return launch_walk<DK, W, NP, 2, 1, IO>(a.p, s);
+  else return launch_walk<DK, W, NP, IO>(a.p, s);
 }
 template <int DK, int W, int NP> hipError_t launch(const PrepArgs& a, hipStream_t s) {
   if constexpr (NP == 1) return launch_io<DK, W, 1, bf16>(a, s);
