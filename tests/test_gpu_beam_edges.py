@@ -120,3 +120,25 @@ def test_pools_of_every_family(family):
     with torch.cuda.stream(torch.cuda.Stream()):
         run(logits, scores, slots, pool=pool)
         run(logits, scores, slots, pool=pool, in_place=True)
+
+
+def test_logits_past_32_bit_offsets():
+    """16400 rows of 131075 bf16 logits, over 2^31 elements: the last requests as in a call of their own."""
+    log("case: beam far logits")
+    B, K, V, tail = 2050, 8, 131075, 3
+    n, m = B * K, tail * K
+    g = torch.Generator(device="cuda")
+    g.manual_seed(600)
+    logits = torch.empty((B, K, V), dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    scores = -3.0 * torch.rand(n, generator=g, device="cuda")
+    i32 = lambda c: torch.zeros(c, dtype=torch.int32, device="cuda")
+    slots = torch.arange(n, dtype=torch.int32, device="cuda")
+    pool = Pool.allocate_gdn(1, n, 1, 16, 32, 1, 4)
+    got = [i32(n), i32(n), torch.zeros(n, device="cuda"), i32(n)]
+    want = [i32(m), i32(m), torch.zeros(m, device="cuda"), i32(m)]
+    pool.beam_step(logits, scores, slots, *got)
+    pool.beam_step(logits[-tail:], scores[-m:].clone(), slots[-m:].clone(), *want)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x[-m:], y) for x, y in zip(got, want))
+    best = logits[-1].double().log_softmax(-1) + scores[-K:].double()[:, None]
+    assert [int(got[1][n - K]), int(got[0][n - K])] == list(divmod(int(best.argmax()), V))

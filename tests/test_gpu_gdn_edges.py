@@ -249,3 +249,65 @@ def test_prefill_rounds_where_it_says_and_nowhere_else(shape):
         err, bound = (gdn_roundings.norm_of_error(x, want) for x in (got, round_to(sim, "bf16")))
         log(f"  {what}: error {err:.3e}, of the rounded form {bound:.3e}")
         assert err <= 1.05 * bound, what
+
+
+def test_drafts_whose_first_state_replaces_the_rows_own():
+    """The state after the first of four tokens goes back into the row's slot, which is read for it, the rest elsewhere."""
+    log("case: gdn multi decode, first state in place")
+    shape, K = (2, 4, 128, 80), 4
+    L = Layer(shape, 4, 12, 231)
+    L.seed_slots([3, 6])
+    slots_in = np.array([3, 6], np.int32)
+    apart, own = np.array([[0, 1, 2, 4], [5, 7, 8, 9]], np.int32), np.array([[3, 1, 2, 4], [6, 7, 8, 9]], np.int32)
+    u, a, b = (dev(x, "bf16") for x in L.rows(2 * K, "bf16"))
+    start = L.pool.ssm.clone(), L.pool.conv.clone()
+    kept = []
+    for out in (apart, own):
+        L.pool.ssm.copy_(start[0]), L.pool.conv.copy_(start[1])
+        o = L.out(2 * K, "bf16")
+        L.pool.gdn_decode_multi(0, L.w, torch.from_numpy(slots_in).cuda(), torch.from_numpy(out).cuda(), *L.pool.split_qkv(u),
+                                a, b, o, slots_in_host=slots_in, slots_out_host=out)
+        torch.cuda.synchronize()
+        at = out.ravel().tolist()
+        kept.append((o, L.pool.ssm[0, at], L.pool.conv[0, at]))
+    assert all(same(x, y) for x, y in zip(*kept))
+
+
+@pytest.mark.parametrize("io,first,second", [("bf16", 100032, 50001), ("f32", 60000, 20001)])
+def test_prefill_past_32_bit_offsets(io, first, second):
+    """Rows and a workspace of more than 2^31 bytes: a sequence behind a very long one is what it is alone, bit for bit."""
+    log(f"case: gdn prefill {first} + {second} wide rows io={io}")
+    L = Layer(SHAPES[-1], 4, 4, 241)
+    T = first + second
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    rows = lambda n: torch.empty((T, n), dtype=torch.bfloat16 if io == "bf16" else torch.float32, device="cuda").normal_(generator=g)
+    u, a, b = rows(L.cd), rows(32), rows(32)
+    q, k, v = L.pool.split_qkv(u)
+    o, alone = L.out(T, io), L.out(second, io)
+    assert L.pool.gdn_workspace_size([0, first, T], io_dtype=o.dtype, o_dtype=o.dtype) > 2 ** 31
+    L.pool.gdn_prefill(0, L.w, [0, first, T], [0, 1], [0, 0], q, k, v, a, b, o)
+    L.pool.gdn_prefill(0, L.w, [0, second], [2], [0], q[first:], k[first:], v[first:], a[first:], b[first:], alone)
+    torch.cuda.synchronize()
+    assert torch.isfinite(alone).all() and alone.float().abs().max() > 0.01
+    assert same(o[first:], alone) and same(L.pool.ssm[0, 1], L.pool.ssm[0, 2]) and same(L.pool.conv[0, 1], L.pool.conv[0, 2])
+
+
+def test_prefill_of_66001_sequences():
+    """One row each; the last ones as in a call of their own, bit for bit, and no slot but theirs is touched."""
+    log("case: gdn prefill 66001 sequences")
+    n, shape = 66001, (1, 1, 32, 16)
+    L = Layer(shape, 4, n + 6, 251)
+    L.pool.ssm.normal_(), L.pool.conv.normal_()
+    u = torch.randn((n, L.cd + 2), device="cuda").bfloat16()
+    q, k, v = L.pool.split_qkv(u[:, :L.cd].contiguous())
+    a, b = u[:, L.cd:L.cd + 1], u[:, L.cd + 1:]
+    for t in (L.pool.ssm, L.pool.conv):
+        t[0, n + 1:] = t[0, n - 5:n]
+    kept = L.pool.ssm[0, n].clone()
+    o, last = L.out(n, "bf16"), L.out(5, "bf16")
+    L.pool.gdn_prefill(0, L.w, np.arange(n + 1), np.arange(n), np.ones(n), q, k, v, a, b, o)
+    L.pool.gdn_prefill(0, L.w, np.arange(6), np.arange(n + 1, n + 6), np.ones(5), q[-5:], k[-5:], v[-5:], a[-5:], b[-5:], last)
+    torch.cuda.synchronize()
+    assert same(o[-5:], last) and same(L.pool.ssm[0, n - 5:n], L.pool.ssm[0, n + 1:]) and same(L.pool.ssm[0, n], kept)
+    assert same(L.pool.conv[0, n - 5:n], L.pool.conv[0, n + 1:])
