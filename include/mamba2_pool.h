@@ -455,8 +455,7 @@ m2_status mamba2_gdn_decode_multi(m2_pool* pool, int32_t layer, const m2_layer_p
                                   int32_t o_dtype, void* stream);
 
 /* Workspace bytes mamba2_gdn_prefill needs for a call with these host arguments
- * and dtypes (fp32 q, k, v or o take 1.4 to 2.6 times the bytes, more the wider dk
- * and the fewer value heads a key head has).  Host-only.
+ * and dtypes (fp32 q, k, v or o take 2.7 to 3 times the bytes).  Host-only.
  * Errors: M2_ERR_ARG, M2_ERR_SHAPE, M2_ERR_DTYPE, M2_ERR_UNSUPPORTED. */
 m2_status mamba2_gdn_prefill_workspace_size(const m2_pool* pool, int32_t num_seqs, const int32_t* cu_seqlens,
                                             const int32_t* start_pos, int32_t ckpt_interval,
@@ -469,9 +468,13 @@ m2_status mamba2_gdn_prefill_workspace_size(const m2_pool* pool, int32_t num_seq
  * and the checkpoint slots.  cu_seqlens, slots, has_initial_state, start_pos,
  * ckpt_interval, ckpt_slots [num_seqs][max_ckpt], zero-length sequences and the
  * launch tables as in mamba2_prefill_chunked; rows behind cu_seqlens[num_seqs]
- * are neither read nor written.  With bf16 q, k, v and o the contractions run in
- * bf16 with fp32 accumulation; with fp32 io_dtype or o_dtype on operands of three
- * bf16 planes (six products each) for fp32-level accuracy.  Inputs are taken as finite: a NaN or an
+ * are neither read nor written.  With bf16 q, k, v and o the contractions run on
+ * fp16 operands with fp32 accumulation, each column of dv in units of its own, so
+ * that o and the states are off by little more than their own rounding at any
+ * magnitude.  Of v less what the state holds for it, what is 2^22 below the largest
+ * of its column and chunk (64 rows) loses digits, and 2^33 below counts as 0.  With
+ * fp32 io_dtype or o_dtype operands are three bf16 planes (six products each) for
+ * fp32-level accuracy.  Inputs are taken as finite: a NaN or an
  * infinity may also reach outputs up to 63 rows ahead of it in its sequence,
  * but not past a checkpoint: the rows up to it, its state and its window are
  * those of the rows before the NaN alone.

@@ -48,9 +48,8 @@ using GdnSeq = SeqEntry;   // first packed row, rows, final slot, seed from slot
 struct GdnChunk {   // one per chunk
   int32_t seq, tau0, len, ckpt_slot;  // entry of its sequence, offset inside it, rows, -1 or a slot
 };
-// Operands of one chunk in the workspace, in 1 KiB pieces as the walk's waves take them, bf16 planes
-// (one, or three whose sum is the fp32 value; T and the masked Q K^T have two at
-// least):
+// Operands of one chunk in the workspace, in 1 KiB pieces as the walk's waves take them: one plane in
+// fp16, or three in bf16 whose sum is the fp32 value:
 //   per key head   K [planes][64/16][dk/16][64 lanes][4]: the 16 x 16 tile (rt, dt) of the rows, lane l
 //                  holds row l % 16, columns 4 (l / 16) ..+3
 //                  Q [planes][64/16][dk/32][64 lanes][8]: MFMA fragments
@@ -61,10 +60,9 @@ struct GdnChunk {   // one per chunk
 constexpr int kGdnTriFrags = 6;
 __host__ __device__ constexpr int gdn_tri(int rt, int ks) { return rt < 2 ? rt : 2 * rt - 2 + ks; }
 constexpr int kGdnSplitPlanes = 3;
-__host__ __device__ constexpr int gdn_t_planes(int planes) { return planes == 1 ? 2 : planes; }
 // bytes per (chunk, key head) and per (chunk, value head)
 __host__ __device__ constexpr int gdn_kq_bytes(int dk, int planes) { return 2 * planes * kGdnChunk * dk * 2; }
-__host__ __device__ constexpr int gdn_t_bytes(int planes) { return (gdn_t_planes(planes) * kGdnTriFrags + 1) * 1024; }
+__host__ __device__ constexpr int gdn_t_bytes(int planes) { return (planes * kGdnTriFrags + 1) * 1024; }
 __host__ __device__ constexpr int gdn_a_bytes(int planes) { return gdn_t_bytes(planes); }
 __host__ __device__ constexpr int gdn_head_bytes(int planes) { return gdn_t_bytes(planes) + gdn_a_bytes(planes); }
 

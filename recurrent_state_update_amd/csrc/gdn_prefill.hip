@@ -19,21 +19,21 @@
 //                   chain S0 -> K S0 -> U -> S1 never leaves a wave's registers.  role_walk_kernel
 //                   for bf16 rows and dk <= 128, walk_kernel otherwise (one wave does all the work
 //                   of its columns).
-// Measured at 32 value heads of 128 x 128 over 16 key heads: 8192 rows of one sequence 303 us (launch 1
-// 82 us: 33 of them VALU issue, 2340 instructions a wave, the rest latency that three workgroups a CU do
-// not cover; it writes 218 MB, 44 of them spilled registers; launch 2 221 us, 1.7 us a chunk), 16 x 1024
-// rows 441 us.
-// Operands are bf16, one plane each, with fp32 accumulation; or, when q, k, v or o are fp32, three
+// Measured at 32 value heads of 128 x 128 over 16 key heads: 8192 rows of one sequence 257 us (launch 1
+// 77 us: 31 of them VALU issue, 2220 instructions a wave, the rest latency that three workgroups a CU do
+// not cover; it writes 168 MB, 44 of them spilled registers; launch 2 189 us, 1.5 us a chunk), 16 x 1024
+// rows 393 us.
+// Operands are fp16, one plane each, with fp32 accumulation; or, when q, k, v or o are fp32, three bf16
 // planes whose sum is the fp32 value, and six MFMAs a product (the terms above 2^-24 of it).
+// fp16 because K, Q, T, the masked Q K^T and the gates are at most 1 and everything else can be put in
+// units (below): its 11 bits leave o and the states 3e-4 of the 2-norm off before their own rounding to
+// bf16, 1.7e-3, 6e-4 where nothing decays.  With bf16 operands, U, e^(G-g) U, T and the masked Q K^T in
+// two planes, it was 1.5e-3 to 2e-3, most of it from K and Q, and 8192 rows took 304 us.
 // What the diagonals of T and Q K^T carry stays fp32 throughout: U starts from the unrounded R, and
 // O takes q_i.k_i u_i elementwise, q_i.k_i from the unrounded rows.  The diagonal terms are the
-// largest of their sums, so this takes the 2-norm error of a bf16 call from 4.2e-3 to 2.9e-3 (of
-// which 1.7e-3 is the rounding of o itself), and costs no product.
-// The masked Q K^T, U and e^(G-g) U have two planes: 2.9e-3 becomes 2.3e-3, for o as for the states,
-// within 1.4 times the rounding that no kernel can avoid; 8192 rows took 311 us instead of 272 for it.
-// T has two planes as well: where keys repeat, U holds differences of neighbouring v whose sum over
-// the chunk must telescope, and T's roundings, each repeated down a column, would add up instead
-// (one key written 150 times without decay: 2.2e-2 of the 2-norm with one plane, 6e-3 with two).
+// largest of their sums, and it costs no product.  Where keys repeat, U holds differences of
+// neighbouring v whose sum over the chunk must telescope, and T's roundings, each repeated down a
+// column, add up instead: one key written 150 times without decay is 2.4e-3 off, rounding included.
 // State, gates, T and all sums are fp32, the sum of log alpha fp64: differences of it far behind a
 // strong decay would lose the digits of the weak ones after it.
 #include <cstddef>
@@ -50,6 +50,9 @@ constexpr int C = kGdnChunk;
 constexpr int kPrepThreads = 256;
 constexpr int LDL = C + 4;            // row pitch of the fp32 C x C matrices in LDS
 constexpr int kTri = kGdnTriFrags * 512;   // elements of a plane of T or of the masked Q K^T
+// In fp16, T and the masked Q K^T, which are at most 1, are stored times 2^15: entries behind a strong decay
+// keep their digits down to 2^-29 and are 0 below 2^-40.  The gates that go with them carry the factor too.
+template <int NP> constexpr float kLift = NP == 1 ? 0x1p15f : 1.f;
 
 struct alignas(16) PrepArgs {   // the first launch's one argument
   GdnPrefillParams p;
@@ -59,33 +62,48 @@ struct alignas(16) PrepArgs {   // the first launch's one argument
 typedef uint16_t u16;
 typedef u16 u16x4 __attribute__((ext_vector_type(4)));
 typedef u16 u16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16;
+typedef f16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float floatx2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ u16 bits(bf16 v) { return __builtin_bit_cast(u16, v); }
-__device__ __forceinline__ bf16x8 frag8(const u16* p) { return *reinterpret_cast<const bf16x8*>(p); }
 
-// An operand in NP bf16 planes, the largest first: each plane is the rounding of what the ones
+// An operand: one plane in fp16, or NP in bf16, the largest first: each is the rounding of what the ones
 // before it leave.
 template <int NP> struct Op {
-  bf16x8 p[NP];
+  typedef bf16x8 vec;
+  vec p[NP];
+};
+template <> struct Op<1> {
+  typedef f16x8 vec;
+  vec p[1];
 };
 template <int NP> __device__ __forceinline__ Op<NP> make_op(const float (&v)[8]) {
   Op<NP> o;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    float rest = v[e];
+    if constexpr (NP == 1) {
+      o.p[0][e] = static_cast<f16>(v[e]);
+    } else {
+      float rest = v[e];
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      o.p[i][e] = from_f32<bf16>(rest);
-      if (i + 1 < NP) rest -= static_cast<float>(o.p[i][e]);
+      for (int i = 0; i < NP; ++i) {
+        o.p[i][e] = from_f32<bf16>(rest);
+        if (i + 1 < NP) rest -= static_cast<float>(o.p[i][e]);
+      }
     }
   }
   return o;
 }
+__device__ __forceinline__ floatx4 mfma(const bf16x8& a, const bf16x8& b, floatx4 acc) { return mfma_bf16(a, b, acc); }
+__device__ __forceinline__ floatx4 mfma(const f16x8& a, const f16x8& b, floatx4 acc) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, acc, 0, 0, 0);
+}
 // acc += a b, without the plane products below 2^-8 per plane of it; the small ones first.
-template <int NA, int NB> __device__ __forceinline__ floatx4 mul(const Op<NA>& a, const Op<NB>& b, floatx4 acc) {
+template <int NP> __device__ __forceinline__ floatx4 mul(const Op<NP>& a, const Op<NP>& b, floatx4 acc) {
 #pragma unroll
-  for (int s = (NA > NB ? NA : NB) - 1; s >= 0; --s)
+  for (int s = NP - 1; s >= 0; --s)
 #pragma unroll
-    for (int i = s < NA ? s : NA - 1; i >= 0 && s - i < NB; --i) acc = mfma_bf16(a.p[i], b.p[s - i], acc);
+    for (int i = s; i >= 0; --i) acc = mfma(a.p[i], b.p[s - i], acc);
   return acc;
 }
 // Waits until MFMA results in flight are in their registers.  The compiler places such waits by
@@ -133,7 +151,7 @@ template <int DK, int NP> struct PrepLds {
 template <int NP> __device__ __forceinline__ Op<NP> lds_op(const u16* p, int gap) {
   Op<1> o;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) o.p[0][e] = __builtin_bit_cast(bf16, p[(e >> 2) * gap + (e & 3)]);
+  for (int e = 0; e < 8; ++e) o.p[0][e] = __builtin_bit_cast(f16, p[(e >> 2) * gap + (e & 3)]);
   return o;
 }
 template <int NP> __device__ __forceinline__ Op<NP> lds_op(const float* p, int gap) {
@@ -145,12 +163,12 @@ template <int NP> __device__ __forceinline__ Op<NP> lds_op(const float* p, int g
 // Lane `lane`'s part of fragment f of an array of planes `plane` elements apart.
 template <int NP> __device__ __forceinline__ void put_op(u16* base, int plane, int f, int lane, const Op<NP>& o) {
 #pragma unroll
-  for (int i = 0; i < NP; ++i) *reinterpret_cast<bf16x8*>(base + i * plane + (f * 64 + lane) * 8) = o.p[i];
+  for (int i = 0; i < NP; ++i) *reinterpret_cast<typename Op<NP>::vec*>(base + i * plane + (f * 64 + lane) * 8) = o.p[i];
 }
 template <int NP> __device__ __forceinline__ Op<NP> get_op(const u16* base, int plane, int f, int lane) {
   Op<NP> o;
 #pragma unroll
-  for (int i = 0; i < NP; ++i) o.p[i] = frag8(base + i * plane + (f * 64 + lane) * 8);
+  for (int i = 0; i < NP; ++i) o.p[i] = *reinterpret_cast<const typename Op<NP>::vec*>(base + i * plane + (f * 64 + lane) * 8);
   return o;
 }
 
@@ -167,7 +185,7 @@ __global__ __launch_bounds__(kPrepThreads) __attribute__((amdgpu_waves_per_eu(3)
 void prep_kernel(PrepArgs args) {
   typedef PrepLds<DK, NP> Lds;
   typedef typename Lds::row_t row_t;
-  constexpr int LDK = Lds::LDK, NPT = gdn_t_planes(NP);
+  constexpr int LDK = Lds::LDK;
   constexpr int LPR = DK / 8, KS = DK / 32, RR = DK / 16;   // lanes a row, K steps, rows a thread
   constexpr int RB = RR < 8 ? RR : 8;                       // rows a thread takes at a time
   const GdnPrefillParams& p = args.p;
@@ -254,7 +272,7 @@ void prep_kernel(PrepArgs args) {
         if (sub == 0 && !isk) s.diag[row] = kq;
         row_t* dst = (isk ? s.k : s.q) + row * LDK + sub * 8;
         if constexpr (NP == 1) {
-          *reinterpret_cast<bf16x8*>(dst) = make_op<1>(act).p[0];
+          *reinterpret_cast<f16x8*>(dst) = make_op<1>(act).p[0];
         } else {
           *reinterpret_cast<floatx4*>(dst) = floatx4{act[0], act[1], act[2], act[3]};
           *reinterpret_cast<floatx4*>(dst + 4) = floatx4{act[4], act[5], act[6], act[7]};
@@ -294,13 +312,13 @@ void prep_kernel(PrepArgs args) {
     }
     const float eg = expf((float)ga);
     u16* const tout = t_of(hl);
-    float* const g1 = reinterpret_cast<float*>(tout + NPT * kTri);
+    float* const g1 = reinterpret_cast<float*>(tout + NP * kTri);
     g1[lane] = be;
     g1[C + lane] = be * eg;
-    g1[2 * C + lane] = expf((float)(G - ga));
+    g1[2 * C + lane] = expf((float)(G - ga)) / kLift<NP>;
     g1[3 * C + lane] = __shfl(eg, 63);
-    float* const g2 = reinterpret_cast<float*>(tout + gdn_t_bytes(NP) / 2 + NPT * kTri);
-    g2[lane] = eg;
+    float* const g2 = reinterpret_cast<float*>(tout + gdn_t_bytes(NP) / 2 + NP * kTri);
+    g2[lane] = eg * kLift<NP>;
   };
   if (wave < 2 && wave < rep) gates(wave, wave);
   __syncthreads();
@@ -348,6 +366,9 @@ void prep_kernel(PrepArgs args) {
   }
   pin(acc);
   settle();
+  acc[1] = acc[1] * kLift<NP>;
+  acc[2] = acc[2] * kLift<NP>;
+  if (zq) acc[0] = acc[0] * kLift<NP>;
 
   // ---------------------------------------------------------------- value heads, two at a time
   for (int h0 = 0; h0 < rep; h0 += 2) {
@@ -359,7 +380,7 @@ void prep_kernel(PrepArgs args) {
     __syncthreads();
     for (int z = 0; z < nh; ++z) {
       u16* const aout = t_of(h0 + z) + gdn_t_bytes(NP) / 2;
-      if (wave == 0) reinterpret_cast<float*>(aout + NPT * kTri)[C + lane] = s.diag[lane];
+      if (wave == 0) reinterpret_cast<float*>(aout + NP * kTri)[C + lane] = s.diag[lane];
       // four values of the tile (it, jt): e^(g_i - g_j) below the diagonal, else 0.  COLS: columns j =
       // 4 q + r of row i = l; else rows i = 4 q + r of column j = l.
       auto decays = [&](int it, int jt, bool cols) {
@@ -386,11 +407,11 @@ void prep_kernel(PrepArgs args) {
       const floatx4 none = {0.f, 0.f, 0.f, 0.f};
       const floatx4 a1 = decays(qi, kj[1], true) * acc[1], a2 = decays(qi, kj[2], true) * acc[2];
       const float pair[8] = {a1[0], a1[1], a1[2], a1[3], a2[0], a2[1], a2[2], a2[3]};
-      put_op<NPT>(aout, kTri, gdn_tri(qi, qp), lane, make_op<NPT>(pair));
+      put_op<NP>(aout, kTri, gdn_tri(qi, qp), lane, make_op<NP>(pair));
       if (zq) {
         const floatx4 a0 = decays(ki[0], ki[0], true) * acc[0];
         const float half[8] = {a0[0], a0[1], a0[2], a0[3], none[0], none[1], none[2], none[3]};
-        put_op<NPT>(aout, kTri, gdn_tri(ki[0], ki[0] / 2), lane, make_op<NPT>(half));
+        put_op<NP>(aout, kTri, gdn_tri(ki[0], ki[0] / 2), lane, make_op<NP>(half));
       } else {
         put_l(0);
       }
@@ -433,7 +454,7 @@ void prep_kernel(PrepArgs args) {
       const float *lt = s.lt[z], *xt = s.xt[z];
       floatx4 Y[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) Y[I][r] = xt[(16 * I + 4 * q4 + r) * 20 + l16];
+      for (int r = 0; r < 4; ++r) Y[I][r] = xt[(16 * I + 4 * q4 + r) * 20 + l16] * kLift<NP>;
 #pragma unroll
       for (int j = I - 1; j >= 0; --j) {
         floatx4 m = {0.f, 0.f, 0.f, 0.f};
@@ -458,7 +479,7 @@ void prep_kernel(PrepArgs args) {
           // the unit diagonal is left out: U takes R itself there
           v[e] = j > I ? 0.f : j == I ? (4 * q4 + (e & 3) < l16 ? Y[I][e & 3] : 0.f) : Y[j][e & 3];
         }
-        put_op<NPT>(tout, kTri, gdn_tri(I, ks), lane, make_op<NPT>(v));
+        put_op<NP>(tout, kTri, gdn_tri(I, ks), lane, make_op<NP>(v));
       }
     };
     // tiles I cost 0, 2, 5 and 9 products: the second head takes them the other way round
@@ -490,13 +511,46 @@ __device__ __forceinline__ void wait_dma() { __builtin_amdgcn_s_waitcnt(0x0f70);
 
 // K^T out of the K tiles by transposing reads: lane l of 16 lanes gets column l of four rows.  `t` is
 // the lane's piece of the tile of the lower 16 rows, `step` elements ahead of that of the upper 16.
-__device__ __forceinline__ bf16x8 tr_frag(const u16* t, int step) {
+template <typename V> __device__ __forceinline__ V tr_frag(const u16* t, int step) {
   typedef short s16x4 __attribute__((ext_vector_type(4)));
   typedef short s16x8 __attribute__((ext_vector_type(8)));
   typedef __attribute__((address_space(3))) s16x4 lds4;
   const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)t);
   const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(t + step));
-  return __builtin_bit_cast(bf16x8, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+  return __builtin_bit_cast(V, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+}
+
+// ---- Units of the fp16 form.  Everything that the walk does to a column of dv is linear in that column of
+// V and S, so its fp16 operands are in units of the column's own, powers of two: S0 in one that puts its
+// largest element between 2^14 and 2^15; R, U and e^(G-g) U in one that puts the largest of R between 2^8 and
+// 2^9.  |k| <= 1 and gates <= 1 bound T by 1, so that |U| <= 64 max |R| < 2^15 in that unit: nothing
+// overflows, and 2^-22 of the largest still has all its digits.
+struct Unit {
+  float size, inverse;
+};
+template <int E> __device__ __forceinline__ Unit unit_of(float largest) {   // largest / size in [2^E, 2^(E+1))
+  const uint32_t e = __float_as_uint(fminf(fmaxf(largest, 0x1p-100f), 0x1p126f)) & 0x7f800000u;   // 2^floor(log2)
+  const uint32_t u = e - ((uint32_t)E << 23);
+  return {__uint_as_float(u), __uint_as_float((254u << 23) - u)};
+}
+// The unit of R.  The next state is in it too: its part from S0, at most `rest`, must not overflow fp32.
+__device__ __forceinline__ Unit unit_of_r(float largest, float rest) { return unit_of<8>(fmaxf(largest, rest * 0x1p-60f)); }
+// A ratio of units, finite, so that what it multiplies stays zero if it is.
+__device__ __forceinline__ float finite(float ratio) { return fminf(ratio, 0x1p127f); }
+// The largest of the four lanes that have a column (lane, lane ^ 16, ^ 32, ^ 48).
+__device__ __forceinline__ float column_max(float v) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+template <int N> __device__ __forceinline__ float largest(const floatx4 (&x)[N]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) m = fmaxf(m, fabsf(x[i][r]));
+  return m;
 }
 
 constexpr int kWalkWaves = 2;   // of a walk_kernel workgroup, 16 columns of dv each
@@ -524,7 +578,7 @@ template <int DK, int NP, typename IO> struct Stage {
 template <int DK, int W, int NP, int NB, typename IO>
 __global__ __launch_bounds__(64 * kWalkWaves) void walk_kernel(GdnPrefillParams p, int parts, int groups) {
   typedef Stage<DK, NP, IO> St;
-  constexpr int KS = DK / 32, NT = DK / 16, NPT = gdn_t_planes(NP);
+  constexpr int KS = DK / 32, NT = DK / 16;
   extern __shared__ char smem[];
   const int lane = threadIdx.x & 63, q4 = lane >> 4, l16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -545,7 +599,8 @@ __global__ __launch_bounds__(64 * kWalkWaves) void walk_kernel(GdnPrefillParams 
   const int col = has ? c0 + l16 : dv - 1;                // a lane without a column repeats the last one
   const int gc = 2 * p.sh.Hk * DK + h * dv + col;         // its conv channel
   float wt[W], win[W - 1];
-  floatx4 S[NT];
+  floatx4 S[NT];      // in units of `unit` (three planes: of 1)
+  float unit = 1.f;
 #pragma unroll
   for (int j = 0; j < W; ++j) wt[j] = p.conv_w[(int64_t)gc * W + j];
   const float bias = p.conv_b ? p.conv_b[gc] : 0.f;
@@ -568,7 +623,7 @@ __global__ __launch_bounds__(64 * kWalkWaves) void walk_kernel(GdnPrefillParams 
       for (int i = 0; i < NT; ++i) {
         u16x4 o;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) o[r] = bits(from_f32<bf16>(S[i][r]));
+        for (int r = 0; r < 4; ++r) o[r] = bits(from_f32<bf16>(S[i][r] * unit));
         *reinterpret_cast<u16x4*>(sp + 16 * i) = o;
       }
       if (q4 == 0) {
@@ -643,36 +698,11 @@ __global__ __launch_bounds__(64 * kWalkWaves) void walk_kernel(GdnPrefillParams 
                                      : reinterpret_cast<const u16*>(p.kq + ((int64_t)c * p.sh.Hk + g) * St::KQ) + NP * C * DK;
       const u16* const Tf = reinterpret_cast<const u16*>(st + St::KIN);
       const u16* const Af = Tf + gdn_t_bytes(NP) / 2;
-      const float* const g1 = reinterpret_cast<const float*>(Tf + NPT * kTri) + 4 * q4;
-      const float* const g2 = reinterpret_cast<const float*>(Af + NPT * kTri) + 4 * q4;
+      const float* const g1 = reinterpret_cast<const float*>(Tf + NP * kTri) + 4 * q4;
+      const float* const g2 = reinterpret_cast<const float*>(Af + NP * kTri) + 4 * q4;
       const IO* const vs = reinterpret_cast<const IO*>(st + St::KIN + St::HEAD + wave * St::V_OPS * 1024) + l16;
-      // K S0 and Q S0
-      floatx4 X[4], Y[4];
-#pragma unroll
-      for (int rt = 0; rt < 4; ++rt) X[rt] = Y[rt] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const Op<NP> sf = acc_op<NP>(S[2 * ks], S[2 * ks + 1]);
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-          Op<NP> k;
-#pragma unroll
-          for (int i = 0; i < NP; ++i) {
-            const u16* t = Kt + i * C * DK + (rt * NT + 2 * ks) * 256 + lane * 4;
-            const u16x4 lo = *reinterpret_cast<const u16x4*>(t), hi = *reinterpret_cast<const u16x4*>(t + 256);
-            k.p[i] = __builtin_bit_cast(bf16x8, u16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
-          }
-          const Op<NP> q = get_op<NP>(Qf, C * DK, rt * KS + ks, lane);
-          X[rt] = mul(k, sf, X[rt]);
-          Y[rt] = mul(q, sf, Y[rt]);
-        }
-      }
-      // R = beta (V - e^g K S0)
-      floatx4 U[4];
-#pragma unroll
-      for (int rt = 0; rt < 4; ++rt) {
-        const floatx4 be = *reinterpret_cast<const floatx4*>(g1 + 16 * rt);
-        const floatx4 bg = *reinterpret_cast<const floatx4*>(g1 + C + 16 * rt);
+      // SiLU(conv) of rows 16 rt + 4 q4 .. +3 of the lane's column
+      auto conv_tile = [&](int rt) {
         float v[W + 3];
 #pragma unroll
         for (int j = 0; j < W + 3; ++j) {
@@ -685,25 +715,76 @@ __global__ __launch_bounds__(64 * kWalkWaves) void walk_kernel(GdnPrefillParams 
           }
           v[j] = x;
         }
+        floatx4 o;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           float x = bias;
 #pragma unroll
           for (int j = 0; j < W; ++j) x += wt[j] * v[r + j];
-          // behind the chunk beta is 0, and the v row, perhaps one of the next chunk, is left out: it may
-          // hold a NaN, which must not reach this chunk's end state
-          const bool inside = 16 * rt + 4 * q4 + r < ce.len;
-          U[rt][r] = be[r] * (inside ? silu(x) : 0.f) - bg[r] * X[rt][r];
+          // a row behind the chunk, perhaps one of the next chunk, may hold a NaN, which must not reach this
+          // chunk's end state
+          o[r] = 16 * rt + 4 * q4 + r < ce.len ? silu(x) : 0.f;
+        }
+        return o;
+      };
+      float most = 0.f;
+      Unit su = {1.f, 1.f};
+      if constexpr (NP == 1) {
+        most = column_max(largest(S));
+        su = unit_of<14>(most);
+      }
+      // K S0 and Q S0
+      floatx4 X[4], Y[4];
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) X[rt] = Y[rt] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const Op<NP> sf = acc_op<NP>(S[2 * ks] * su.inverse, S[2 * ks + 1] * su.inverse);
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+          Op<NP> k;
+#pragma unroll
+          for (int i = 0; i < NP; ++i) {
+            const u16* t = Kt + i * C * DK + (rt * NT + 2 * ks) * 256 + lane * 4;
+            const u16x4 lo = *reinterpret_cast<const u16x4*>(t), hi = *reinterpret_cast<const u16x4*>(t + 256);
+            k.p[i] = __builtin_bit_cast(typename Op<NP>::vec, u16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+          }
+          const Op<NP> q = get_op<NP>(Qf, C * DK, rt * KS + ks, lane);
+          X[rt] = mul(k, sf, X[rt]);
+          Y[rt] = mul(q, sf, Y[rt]);
         }
       }
+      // R = beta (V - e^g K S0)
+      const float xs = NP == 1 ? su.size * unit : 1.f;
+      floatx4 U[4];
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) {
+        const floatx4 be = *reinterpret_cast<const floatx4*>(g1 + 16 * rt);
+        const floatx4 bg = *reinterpret_cast<const floatx4*>(g1 + C + 16 * rt);
+        U[rt] = be * conv_tile(rt) - bg * (X[rt] * xs);    // beta is 0 behind the chunk
+      }
+      // from here on R, U, the state and, lifted, O are in the column's unit
+      const float decay = g1[3 * C];
+      Unit ru = {1.f, 1.f};
+      if constexpr (NP == 1) ru = unit_of_r(column_max(largest(U)), decay * most * unit);
+      const float keep = NP == 1 ? decay * finite(unit * ru.inverse) : decay, ratio = NP == 1 ? finite(xs * ru.inverse) : 1.f;
+      unit = NP == 1 ? ru.size : 1.f;
       // U = R + (T - I) R
       {
+        if constexpr (NP == 1) {
+#pragma unroll
+          for (int rt = 0; rt < 4; ++rt) U[rt] = U[rt] * ru.inverse;
+        }
         const Op<NP> rf[2] = {acc_op<NP>(U[0], U[1]), acc_op<NP>(U[2], U[3])};
+        if constexpr (NP == 1) {
+#pragma unroll
+          for (int rt = 0; rt < 4; ++rt) U[rt] = U[rt] * kLift<NP>;
+        }
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
           for (int ks = 0; ks <= rt / 2; ++ks) {
-            const Op<NPT> t = get_op<NPT>(Tf, kTri, gdn_tri(rt, ks), lane);
+            const Op<NP> t = get_op<NP>(Tf, kTri, gdn_tri(rt, ks), lane);
             U[rt] = mul(t, rf[ks], U[rt]);
           }
       }
@@ -715,32 +796,32 @@ __global__ __launch_bounds__(64 * kWalkWaves) void walk_kernel(GdnPrefillParams 
           const floatx4 eG = *reinterpret_cast<const floatx4*>(g1 + 2 * C + 16 * rt);
           w[rt] = U[rt] * eG;
         }
-        const Op<NPT> uf[2] = {acc_op<NPT>(w[0], w[1]), acc_op<NPT>(w[2], w[3])};
-        const float decay = g1[3 * C];
+        const Op<NP> uf[2] = {acc_op<NP>(w[0], w[1]), acc_op<NP>(w[2], w[3])};
         const u16* const tr = Kt + ((l16 & 3) * 16 + 4 * q4 + (l16 >> 2)) * 4;
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-          S[i] = S[i] * decay;
+          S[i] = S[i] * keep;
 #pragma unroll
           for (int ks = 0; ks < 2; ++ks) {
             Op<NP> k;
 #pragma unroll
-            for (int pl = 0; pl < NP; ++pl) k.p[pl] = tr_frag(tr + pl * C * DK + (2 * ks * NT + i) * 256, NT * 256);
+            for (int pl = 0; pl < NP; ++pl) k.p[pl] = tr_frag<typename Op<NP>::vec>(tr + pl * C * DK + (2 * ks * NT + i) * 256, NT * 256);
             S[i] = mul(k, uf[ks], S[i]);
           }
         }
       }
       // O = e^g Q S0 + q.k U + (Q K^T below the diagonal) U
       {
-        const Op<NPT> uf[2] = {acc_op<NPT>(U[0], U[1]), acc_op<NPT>(U[2], U[3])};
+        constexpr float lower = 1.f / kLift<NP>;
+        const Op<NP> uf[2] = {acc_op<NP>(U[0] * lower, U[1] * lower), acc_op<NP>(U[2] * lower, U[3] * lower)};
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
           const floatx4 eg = *reinterpret_cast<const floatx4*>(g2 + 16 * rt);
           const floatx4 qk = *reinterpret_cast<const floatx4*>(g2 + C + 16 * rt);
-          Y[rt] = eg * Y[rt] + qk * U[rt];
+          Y[rt] = eg * (Y[rt] * ratio) + qk * U[rt];
 #pragma unroll
           for (int ks = 0; ks <= rt / 2; ++ks) {
-            const Op<NPT> a = get_op<NPT>(Af, kTri, gdn_tri(rt, ks), lane);
+            const Op<NP> a = get_op<NP>(Af, kTri, gdn_tri(rt, ks), lane);
             Y[rt] = mul(a, uf[ks], Y[rt]);
           }
         }
@@ -755,7 +836,7 @@ __global__ __launch_bounds__(64 * kWalkWaves) void walk_kernel(GdnPrefillParams 
           const int i = 16 * rt + 4 * q4 + r;
           if (i < ce.len) {
             const int64_t at = ((int64_t)se.t0 + ce.tau0 + i) * p.o_stride + h * dv;
-            if (has) store_any(p.o, at + col, Y[rt][r], NP == 1 ? 1 : p.o_bf16);
+            if (has) store_any(p.o, at + col, Y[rt][r] * (unit / kLift<NP>), NP == 1 ? 1 : p.o_bf16);
           }
         }
       if (ce.ckpt_slot >= 0) put_slot(ce.ckpt_slot, ce.tau0 + ce.len);
@@ -791,21 +872,23 @@ template <int DK, int W, int NP, typename IO> hipError_t launch_walk(const GdnPr
 //   waves 4-7  conv and SiLU of the v rows of chunk n+1, 16 rows each, and the windows of slots.
 // Waves 2-7 also copy the operands of the next step from the workspace to LDS.  One barrier a step.
 // The columns of tile ct are 2 l + ct, so that an output lane has two adjacent ones.
-// Measured on 8192 rows of one sequence (128 workgroups): 1.7 us a step, bound by the instructions
-// of the chain (60 MFMAs, 20 deep, between 88 LDS accesses) and what waits for the copies and the
-// barrier.  With one plane of U and of Q K^T 1.4 us; then one wave doing all the work of 16 columns
-// took 4.2 us, these roles with the loads left to the compiler's order 2.7 us, and ten or twelve waves,
-// which leave a wave 168 registers instead of 256, 2.0 us and more.  LDS is full (156 KB at dk 128),
-// so that the next workgroup of a CU starts when this one ends.
+// Measured on 8192 rows of one sequence (128 workgroups): 1.5 us a step, bound by the instructions
+// of the chain (38 MFMAs, two searches for a column's largest, some 95 LDS accesses) and what waits for
+// the copies and the barrier.  With bf16 operands, T, U and Q K^T in two planes 1.7 us, in one plane 1.4 us;
+// in that form one wave doing all the work of 16 columns took 4.2 us, these roles with the loads left to
+// the compiler's order 2.7 us, and ten or twelve waves, which leave a wave 168 registers instead of
+// 256, 2.0 us and more.  One workgroup's LDS is 133 KB at dk 128, so that the next one of a CU starts
+// when this one ends.
 template <int DK> struct Roles {
   static constexpr int A = 2 * C * DK + gdn_t_bytes(1);       // K, T, gates: the chain's, per chunk
   static constexpr int B = 2 * C * DK + gdn_a_bytes(1);       // Q, Q K^T, gates: the output's
-  static constexpr int V = 2 * C * 16 * 4;                    // v rows [ct][64/16][64 lanes][4], then U
+  static constexpr int V = 2 * C * 16 * 4;                    // v rows [ct][64/16][64 lanes][4], then U, lifted
   static constexpr int S = 2 * DK * 16 * 2;                   // S0 operands [ct][dk/32][64 lanes][8]
+  static constexpr int UN = 2 * 16 * 8;                       // [ct][16]: S0's unit in U's, and that of the lifted output
   // three places for v rows: the chain puts U where it found them, and the output reads that a step
   // later, while the rows after the next come in
-  static constexpr int OFF_B = 2 * A, OFF_V = OFF_B + 2 * B, OFF_S = OFF_V + 3 * V;
-  static constexpr int BYTES = OFF_S + 2 * S;
+  static constexpr int OFF_B = 2 * A, OFF_V = OFF_B + 2 * B, OFF_S = OFF_V + 3 * V, OFF_UN = OFF_S + 2 * S;
+  static constexpr int BYTES = OFF_UN + 2 * UN;
   static_assert(BYTES <= (int)kMaxLdsBytes && A % 1024 == 0 && B % 1024 == 0, "LDS of a role walk workgroup");
 };
 
@@ -871,13 +954,14 @@ __device__ __forceinline__ void fence_order() { __builtin_amdgcn_sched_barrier(0
 
 template <int DK> __device__ __forceinline__ void chain_role(const GdnPrefillParams& p, const RoleUnit& u) {
   typedef Roles<DK> Ro;
-  constexpr int KS = DK / 32, NT = DK / 16, NPT = gdn_t_planes(1);
+  constexpr int KS = DK / 32, NT = DK / 16;
   const GdnSeq& se = u.se;
   const int lane = u.lane, q4 = u.q4, l16 = u.l16, dv = p.sh.dv;
   const int col = u.c0 + 2 * l16 + u.wave;
   const bool has = col < dv;
   bf16* const ssm = static_cast<bf16*>(p.ssm);
-  floatx4 S[NT];
+  floatx4 S[NT];      // in units of `unit`
+  float unit = 1.f;
   {
     const bf16* sp = ssm + (((int64_t)se.slot * p.sh.Hv + u.h) * dv + (has ? col : dv - 1)) * DK + 4 * q4;
 #pragma unroll
@@ -894,7 +978,7 @@ template <int DK> __device__ __forceinline__ void chain_role(const GdnPrefillPar
     for (int i = 0; i < NT; ++i) {
       u16x4 o;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) o[r] = bits(from_f32<bf16>(S[i][r]));
+      for (int r = 0; r < 4; ++r) o[r] = bits(from_f32<bf16>(S[i][r] * unit));
       *reinterpret_cast<u16x4*>(sp + 16 * i) = o;
     }
   };
@@ -912,7 +996,7 @@ template <int DK> __device__ __forceinline__ void chain_role(const GdnPrefillPar
     const u16* const Kt = reinterpret_cast<const u16*>(sa) + lane * 4;
     const u16* const tr = reinterpret_cast<const u16*>(sa) + ((l16 & 3) * 16 + 4 * q4 + (l16 >> 2)) * 4;
     const u16* const Tf = reinterpret_cast<const u16*>(sa) + C * DK;
-    const float* const g1 = reinterpret_cast<const float*>(Tf + NPT * kTri) + 4 * q4;
+    const float* const g1 = reinterpret_cast<const float*>(Tf + kTri) + 4 * q4;
     char* const vs = u.smem + Ro::OFF_V + n % 3 * Ro::V + (u.wave * 4 * 64 + lane) * 16;
     u16* const sf = reinterpret_cast<u16*>(u.smem + Ro::OFF_S + now * Ro::S) + (u.wave * KS * 64 + lane) * 8;
     u16x8 k[KS][4];
@@ -924,11 +1008,14 @@ template <int DK> __device__ __forceinline__ void chain_role(const GdnPrefillPar
         const u16x4 lo = *reinterpret_cast<const u16x4*>(t), hi = *reinterpret_cast<const u16x4*>(t + 256);
         k[ks][rt] = u16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
       }
-    bf16x8 s0[KS];
+    const float most = column_max(largest(S));
+    const Unit su = unit_of<14>(most);
+    const float xs = su.size * unit;
+    f16x8 s0[KS];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      s0[ks] = acc_op<1>(S[2 * ks], S[2 * ks + 1]).p[0];
-      *reinterpret_cast<bf16x8*>(sf + ks * 512) = s0[ks];
+      s0[ks] = acc_op<1>(S[2 * ks] * su.inverse, S[2 * ks + 1] * su.inverse).p[0];
+      *reinterpret_cast<f16x8*>(sf + ks * 512) = s0[ks];
     }
     fence_order();
     floatx4 be[4], bg[4], eG[4], v[4];
@@ -945,73 +1032,57 @@ template <int DK> __device__ __forceinline__ void chain_role(const GdnPrefillPar
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-      for (int rt = 0; rt < 4; ++rt) X[rt] = mfma_bf16(__builtin_bit_cast(bf16x8, k[ks][rt]), s0[ks], X[rt]);
+      for (int rt = 0; rt < 4; ++rt) X[rt] = mfma(__builtin_bit_cast(f16x8, k[ks][rt]), s0[ks], X[rt]);
     fence_order();
-    Op<NPT> t[kGdnTriFrags];
+    Op<1> t[kGdnTriFrags];
 #pragma unroll
-    for (int f = 0; f < kGdnTriFrags; ++f) t[f] = get_op<NPT>(Tf, kTri, f, lane);
+    for (int f = 0; f < kGdnTriFrags; ++f) t[f] = get_op<1>(Tf, kTri, f, lane);
     fence_order();
     floatx4 U[4];
 #pragma unroll
-    for (int rt = 0; rt < 4; ++rt) U[rt] = be[rt] * v[rt] - bg[rt] * X[rt];   // R; beta is 0 behind the chunk
-    const Op<1> r0 = acc_op<1>(U[0], U[1]), r1 = acc_op<1>(U[2], U[3]);
+    for (int rt = 0; rt < 4; ++rt) U[rt] = be[rt] * v[rt] - bg[rt] * (X[rt] * xs);   // R; beta is 0 behind the chunk
+    // from here on R, U, the state and, lifted, O are in the column's unit
     const float decay = g1[3 * C];
+    const Unit ru = unit_of_r(column_max(largest(U)), decay * most * unit);
+    const float keep = decay * finite(unit * ru.inverse);
+    unit = ru.size;
+    if (q4 == 0)
+      *reinterpret_cast<floatx2*>(u.smem + Ro::OFF_UN + now * Ro::UN + (u.wave * 16 + l16) * 8) =
+          floatx2{finite(xs * ru.inverse), unit / kLift<1>};
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) U[rt] = U[rt] * ru.inverse;
+    const Op<1> r0 = acc_op<1>(U[0], U[1]), r1 = acc_op<1>(U[2], U[3]);
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) U[rt] = U[rt] * kLift<1>;
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) eG[rt] = *reinterpret_cast<const floatx4*>(g1 + 2 * C + 16 * rt);
     fence_order();
     // T R in an order that keeps products of one sum apart
-#pragma unroll
-    for (int pl = NPT - 1; pl >= 0; --pl) {
-      U[0] = mfma_bf16(t[0].p[pl], r0.p[0], U[0]);
-      U[1] = mfma_bf16(t[1].p[pl], r0.p[0], U[1]);
-      U[2] = mfma_bf16(t[2].p[pl], r0.p[0], U[2]);
-      U[3] = mfma_bf16(t[4].p[pl], r0.p[0], U[3]);
-      U[2] = mfma_bf16(t[3].p[pl], r1.p[0], U[2]);
-      U[3] = mfma_bf16(t[5].p[pl], r1.p[0], U[3]);
-    }
-    bf16x8 kt[2][NT];
+    U[0] = mul(t[0], r0, U[0]);
+    U[1] = mul(t[1], r0, U[1]);
+    U[2] = mul(t[2], r0, U[2]);
+    U[3] = mul(t[4], r0, U[3]);
+    U[2] = mul(t[3], r1, U[2]);
+    U[3] = mul(t[5], r1, U[3]);
+    f16x8 kt[2][NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) kt[ks][i] = tr_frag(tr + (2 * ks * NT + i) * 256, NT * 256);
+      for (int ks = 0; ks < 2; ++ks) kt[ks][i] = tr_frag<f16x8>(tr + (2 * ks * NT + i) * 256, NT * 256);
 #pragma unroll
-    for (int i = 0; i < NT; ++i) S[i] = S[i] * decay;
+    for (int i = 0; i < NT; ++i) S[i] = S[i] * keep;
     fence_order();
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) {
       *reinterpret_cast<floatx4*>(vs + rt * 1024) = U[rt];
       U[rt] = U[rt] * eG[rt];
     }
-    // e^(G-g) U in two planes: the second one is worked out between the products of the first
-    bf16x8 w[2];
-    float rest[2][8];
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        rest[ks][e] = U[2 * ks + (e >> 2)][e & 3];
-        w[ks][e] = from_f32<bf16>(rest[ks][e]);
-      }
+    const Op<1> w[2] = {acc_op<1>(U[0], U[1]), acc_op<1>(U[2], U[3])};
     fence_order();
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-      for (int i = 0; i < NT; ++i) S[i] = mfma_bf16(kt[ks][i], w[ks], S[i]);
-    bf16x8 lo[2];
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) lo[ks][e] = from_f32<bf16>(rest[ks][e] - static_cast<float>(w[ks][e]));
-#pragma unroll
-    for (int i = 0; i < 2 * NT; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);   // a product,
-      __builtin_amdgcn_sched_group_barrier(0x2, 3, 0);   // three vector instructions
-    }
-    fence_order();
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-      for (int i = 0; i < NT; ++i) S[i] = mfma_bf16(kt[ks][i], lo[ks], S[i]);
+      for (int i = 0; i < NT; ++i) S[i] = mfma(kt[ks][i], w[ks].p[0], S[i]);
     pin(S);
     settle();
     if (ckpt >= 0) put_state(ckpt);
@@ -1024,7 +1095,7 @@ template <int DK> __device__ __forceinline__ void chain_role(const GdnPrefillPar
 
 template <int DK, int WHO> __device__ __forceinline__ void output_role(const GdnPrefillParams& p, const RoleUnit& u) {
   typedef Roles<DK> Ro;
-  constexpr int KS = DK / 32, NPT = gdn_t_planes(1);
+  constexpr int KS = DK / 32;
   const GdnSeq& se = u.se;
   const int lane = u.lane, q4 = u.q4;
   // row tiles 0 and 3, or 1 and 2: three fragments of the masked Q K^T either way
@@ -1067,16 +1138,16 @@ template <int DK, int WHO> __device__ __forceinline__ void output_role(const Gdn
       const char* const sb = u.smem + Ro::OFF_B + was * Ro::B;
       const u16* const Qf = reinterpret_cast<const u16*>(sb);
       const u16* const Af = Qf + C * DK;
-      const float* const g2 = reinterpret_cast<const float*>(Af + NPT * kTri) + 4 * q4;
+      const float* const g2 = reinterpret_cast<const float*>(Af + kTri) + 4 * q4;
       const u16* const sf = reinterpret_cast<const u16*>(u.smem + Ro::OFF_S + was * Ro::S);
       const char* const uf = u.smem + Ro::OFF_V + (n - 1) % 3 * Ro::V;
-      bf16x8 s0[KS][2], q[KS][2];
+      f16x8 s0[KS][2], q[KS][2];
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          s0[ks][t] = frag8(sf + ((t * KS + ks) * 64 + lane) * 8);
-          q[ks][t] = frag8(Qf + ((RT[t] * KS + ks) * 64 + lane) * 8);
+          s0[ks][t] = get_op<1>(sf, 0, t * KS + ks, lane).p[0];
+          q[ks][t] = get_op<1>(Qf, 0, RT[t] * KS + ks, lane).p[0];
         }
       fence_order();
       store_out();
@@ -1088,9 +1159,13 @@ template <int DK, int WHO> __device__ __forceinline__ void output_role(const Gdn
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-          for (int ct = 0; ct < 2; ++ct) Y[t][ct] = mfma_bf16(q[ks][t], s0[ks][ct], Y[t][ct]);
+          for (int ct = 0; ct < 2; ++ct) Y[t][ct] = mfma(q[ks][t], s0[ks][ct], Y[t][ct]);
       floatx4 U[2][4], eg[2], qk[2];
-      Op<NPT> a[2], a1;
+      floatx2 unit[2];   // S0's in U's, and that of the output
+      Op<1> a[2], a1;
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct)
+        unit[ct] = *reinterpret_cast<const floatx2*>(u.smem + Ro::OFF_UN + was * Ro::UN + (ct * 16 + u.l16) * 8);
 #pragma unroll
       for (int ct = 0; ct < 2; ++ct)
 #pragma unroll
@@ -1101,19 +1176,20 @@ template <int DK, int WHO> __device__ __forceinline__ void output_role(const Gdn
         const int rt = RT[t];
         eg[t] = *reinterpret_cast<const floatx4*>(g2 + 16 * rt);
         qk[t] = *reinterpret_cast<const floatx4*>(g2 + C + 16 * rt);
-        a[t] = get_op<NPT>(Af, kTri, gdn_tri(rt, 0), lane);
+        a[t] = get_op<1>(Af, kTri, gdn_tri(rt, 0), lane);
       }
-      a1 = get_op<NPT>(Af, kTri, gdn_tri(RT[1], 1), lane);
+      a1 = get_op<1>(Af, kTri, gdn_tri(RT[1], 1), lane);
       fence_order();
 #pragma unroll
       for (int ct = 0; ct < 2; ++ct) {
-        const Op<NPT> u0 = acc_op<NPT>(U[ct][0], U[ct][1]);
+        constexpr float lower = 1.f / kLift<1>;
+        const Op<1> u0 = acc_op<1>(U[ct][0] * lower, U[ct][1] * lower);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          Y[t][ct] = eg[t] * Y[t][ct] + qk[t] * U[ct][RT[t]];
+          Y[t][ct] = eg[t] * (Y[t][ct] * unit[ct][0]) + qk[t] * U[ct][RT[t]];
           Y[t][ct] = mul(a[t], u0, Y[t][ct]);
         }
-        Y[1][ct] = mul(a1, acc_op<NPT>(U[ct][2], U[ct][3]), Y[1][ct]);
+        Y[1][ct] = mul(a1, acc_op<1>(U[ct][2] * lower, U[ct][3] * lower), Y[1][ct]);
       }
       pin(Y[0]);
       pin(Y[1]);
@@ -1122,7 +1198,8 @@ template <int DK, int WHO> __device__ __forceinline__ void output_role(const Gdn
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          out[t][r] = bits(from_f32<bf16>(Y[t][0][r])) | (uint32_t)bits(from_f32<bf16>(Y[t][1][r])) << 16;
+          out[t][r] = bits(from_f32<bf16>(Y[t][0][r] * unit[0][1])) |
+                      (uint32_t)bits(from_f32<bf16>(Y[t][1][r] * unit[1][1])) << 16;
       row = (int64_t)se.t0 + ce.tau0;
       len = ce.len;
     }

@@ -78,7 +78,7 @@ def test_workspace_of_fp32_rows_against_bf16_rows():
         pool = Pool.allocate_gdn(1, 1, hv, 16, dk, hk, 4, device="cpu")
         size = lambda dt: pool.gdn_workspace_size([0, 64 * 400], io_dtype=dt, o_dtype=dt)
         ratio.append(size(torch.float32) / size(torch.bfloat16))
-    assert 1.4 <= min(ratio) and max(ratio) <= 2.6 and 2.0 < ratio[1] < 2.1, ratio
+    assert 2.7 <= min(ratio) and max(ratio) <= 3.0, ratio
 
 
 @pytest.mark.parametrize("heads,code", [(42, OK), (43, UNSUP)])

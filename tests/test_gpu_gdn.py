@@ -4,11 +4,10 @@ Tolerances.  A rounding to bf16 is off by at most 2^-8 of the value.  Decode com
 element of o is off by that rounding (fp32 outputs: none), one of the stored state by twice that
 (the oracle's is rounded too), plus fp32 rounding, whose
 sums over dk <= 256 products and few-ulp exp, reciprocal and root stay below 2^-24 * 300 < 2e-5 of the
-largest value.  The prefill's contractions take bf16 operands: K, Q, S0 and R are rounded once each (T, U,
-e^(G-g) U and the masked Q K^T to two planes), and an error of the state comes back through the next chunk's
-K S0 and Q S0; the relative rms of one rounding is 2^-8 / sqrt(3) * 0.72 = 1.6e-3, and the bound leaves room for
-about 25 independent contributions of weight one: 5 * 1.6e-3 = 8e-3 of the 2-norm.  (test_gpu_gdn_edges.py holds
-the error to that of these roundings alone, about 2.3e-3 with the output's.)  With fp32 rows or
+largest value.  The prefill's contractions take operands of fewer bits: with one rounding to bf16 each, whose relative
+rms is 2^-8 / sqrt(3) * 0.72 = 1.6e-3, about 25 independent contributions of weight one would give 5 * 1.6e-3 = 8e-3 of
+the 2-norm, the bound here; they are fp16, an eighth of that each, and test_gpu_gdn_edges.py holds the error to that of
+these roundings alone, about 1.7e-3 with the output's own.  With fp32 rows or
 outputs an operand is three planes, off by 2^-24, as are products: the fp32 rule holds, of the 2-norm.
 Single elements: six times the 2-norm bound, taken of the largest value.
 """

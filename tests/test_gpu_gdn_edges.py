@@ -233,8 +233,8 @@ def test_prefill_rounds_where_it_says_and_nowhere_else(shape):
     """bf16 rows: the 2-norm error of o and of the state against that of a CPU form in fp64 with roundings at the same
     places of the same values.  fp32 arithmetic takes a value over a rounding border now and then, which changes single
     errors and not their size: of the n > 3000 elements each norm is one of n errors that are independent in the main, so
-    it varies by 1/sqrt(2 n) < 1.3%, and 5% is four times that.  One rounding more, such as U or the masked Q K^T in one
-    plane, adds 10% at least (tests/test_gdn_cpu_roundings.py)."""
+    it varies by 1/sqrt(2 n) < 1.3%, and 5% is four times that.  A bf16 operand in the place of an fp16 one adds 10% at
+    least, for K, Q, R, the masked Q K^T, U or e^(G-g) U (test_gdn_cpu_roundings.py)."""
     log(f"case: gdn prefill roundings {shape}")
     T = 500
     L = Layer(shape, 4, 3, 221)
@@ -311,3 +311,87 @@ def test_prefill_of_66001_sequences():
     torch.cuda.synchronize()
     assert same(o[-5:], last) and same(L.pool.ssm[0, n - 5:n], L.pool.ssm[0, n + 1:]) and same(L.pool.ssm[0, n], kept)
     assert same(L.pool.conv[0, n - 5:n], L.pool.conv[0, n + 1:])
+
+
+def scaled_columns(shape, T, seed, column, row):
+    """A layer whose v reaches the recurrence as SiLU(u) (a conv of one tap), with column c of it times column[c] and row
+    t times row[t]; one sequence from a random state, scaled by column too."""
+    Hk, Hv, dk, dv = shape
+    L = Layer(shape, 4, 3, seed, bias=False)
+    qk = 2 * Hk * dk
+    L.params["conv_w"][qk:] = [0, 0, 0, 1]
+    L.w.conv_w[qk:] = torch.tensor([0.0, 0.0, 0.0, 1.0], device="cuda")
+    L.ssm[1] = round_to(L.rng.normal(0, 0.1, L.ssm[1].shape) * column.reshape(Hv, dv, 1), "bf16")
+    L.conv[1] = 0
+    L.pool.ssm[0, 1], L.pool.conv[0, 1] = torch.from_numpy(L.ssm[1]).to(torch.bfloat16).cuda(), 0
+    u, a, b = L.rows(T, "bf16")
+    u[:, qk:] = round_to(u[:, qk:] * column * row[:, None], "bf16")
+    o = L.out(T, "bf16")
+    q, k, v = L.pool.split_qkv(dev(u, "bf16"))
+    L.pool.gdn_prefill(0, L.w, [0, T], [1], [1], q, k, v, dev(a, "bf16"), dev(b, "bf16"), o)
+    torch.cuda.synchronize()
+    ref = orc.prefill(shape, L.ssm, L.conv, L.params, np.array([0, T]), [1], [1], None, u, a, b)
+    return host(o), ref, host(L.pool.ssm[0, 1]), L.ssm[1]
+
+
+# One element's own rounding is off by 2^-8 at most; the fp16 operands add 3e-4 of the 2-norm on usual rows, and 2e-3 is
+# what the worst conditioned ones (keys that repeat) come to.
+COLUMN_2NORM = 2.0 ** -8 + 2e-3
+
+
+def rel(got, ref, axis):
+    return np.sqrt(((got - ref) ** 2).sum(axis) / np.maximum((ref ** 2).sum(axis), 1e-300))
+
+
+@pytest.mark.parametrize("shape", [(1, 2, 64, 48), (2, 2, 128, 32), (1, 1, 256, 32)], ids=str)
+def test_prefill_columns_of_any_magnitude(shape):
+    """Columns of v and of the state from 1e-25 to 1e30, one of zeros among them: each as exact as the others."""
+    log(f"case: gdn prefill columns of many magnitudes {shape}")
+    n = shape[1] * shape[3]
+    column = 10.0 ** np.linspace(-25, 30, n)
+    column[n // 2] = 0.0
+    o, ref, s, want = scaled_columns(shape, 150, 261, column, np.ones(150))
+    live = np.arange(n) != n // 2
+    assert not o[:, ~live].any() and not s.reshape(n, -1)[~live].any() and np.isfinite(o).all()
+    assert rel(o, ref, 0)[live].max() <= COLUMN_2NORM
+    assert rel(s, want, -1).reshape(-1)[live].max() <= COLUMN_2NORM
+
+
+@pytest.mark.parametrize("shape", [(1, 2, 64, 48), (1, 1, 256, 32)], ids=str)
+def test_prefill_rows_of_many_magnitudes(shape):
+    """v that grows by 1e5 inside a chunk, shrinks by 1e5 in the next, and goes on from there: every row is as exact as
+    its own size asks, also next to rows that set the unit of its chunk."""
+    log(f"case: gdn prefill rows of many magnitudes {shape}")
+    T = 260
+    row = np.ones(T)
+    row[:40] = 1e-5
+    row[40:90] = 1.0
+    row[90:] = 1e-5
+    o, ref, s, want = scaled_columns(shape, T, 271, np.full(shape[1] * shape[3], 1e-3), row)
+    assert rel(o, ref, 1).max() <= COLUMN_2NORM and rel(s.ravel(), want.ravel(), 0) <= COLUMN_2NORM
+
+
+def test_prefill_goes_on_from_a_wiped_state():
+    """Huge rows, then a state that alpha = 0 wipes to exactly nothing, then tiny rows: the unit falls by 2^100."""
+    log("case: gdn prefill wiped state")
+    for shape in ((1, 1, 64, 32), (1, 1, 256, 32)):
+        Hk, Hv, dk, dv = shape
+        L = Layer(shape, 4, 3, 281, bias=False)
+        T = 200
+        L.params["conv_w"][2 * dk:] = [0, 0, 0, 1]
+        L.w.conv_w[2 * dk:] = torch.tensor([0.0, 0.0, 0.0, 1.0], device="cuda")
+        u, a, b = L.rows(T, "bf16")
+        u[:64, 2 * dk:] = round_to(u[:64, 2 * dk:] * 1e15, "bf16")
+        u[64:, 2 * dk:] = round_to(u[64:, 2 * dk:] * 1e-15, "bf16")
+        u[100:140, 2 * dk:] = 0.0
+        a[64:72] = 3e4
+        b[64:68] = -200.0                             # beta is 0: nothing is written either
+        o = L.out(T, "bf16")
+        L.pool.gdn_prefill(0, L.w, [0, T], [1], [0], *L.pool.split_qkv(dev(u, "bf16")), dev(a, "bf16"), dev(b, "bf16"), o)
+        torch.cuda.synchronize()
+        ref = orc.prefill(shape, L.ssm, L.conv, L.params, np.array([0, T]), [1], [0], None, u, a, b)
+        got = host(o)
+        assert not got[64:68].any()
+        for part in (slice(0, 64), slice(68, T)):
+            assert rel(got[part].ravel(), ref[part].ravel(), 0) <= COLUMN_2NORM
+        assert rel(host(L.pool.ssm[0, 1]).ravel(), L.ssm[1].ravel(), 0) <= COLUMN_2NORM
