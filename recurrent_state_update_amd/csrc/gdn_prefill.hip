@@ -51,7 +51,8 @@ constexpr int kPrepThreads = 256;
 constexpr int LDL = C + 4;            // row pitch of the fp32 C x C matrices in LDS
 constexpr int kTri = kGdnTriFrags * 512;   // elements of a plane of T or of the masked Q K^T
 // In fp16, T and the masked Q K^T, which are at most 1, are stored times 2^15: entries behind a strong decay
-// keep their digits down to 2^-29 and are 0 below 2^-40.  The gates that go with them carry the factor too.
+// keep their digits down to 2^-29 and are 0 below 2^-40.  The factor goes on in U, and ends in the gates of
+// the state and in the output's unit.
 template <int NP> constexpr float kLift = NP == 1 ? 0x1p15f : 1.f;
 
 struct alignas(16) PrepArgs {   // the first launch's one argument
@@ -318,7 +319,7 @@ void prep_kernel(PrepArgs args) {
     g1[2 * C + lane] = expf((float)(G - ga)) / kLift<NP>;
     g1[3 * C + lane] = __shfl(eg, 63);
     float* const g2 = reinterpret_cast<float*>(tout + gdn_t_bytes(NP) / 2 + NP * kTri);
-    g2[lane] = eg * kLift<NP>;
+    g2[lane] = eg;
   };
   if (wave < 2 && wave < rep) gates(wave, wave);
   __syncthreads();
@@ -533,8 +534,9 @@ template <int E> __device__ __forceinline__ Unit unit_of(float largest) {   // l
   const uint32_t u = e - ((uint32_t)E << 23);
   return {__uint_as_float(u), __uint_as_float((254u << 23) - u)};
 }
-// The unit of R.  The next state is in it too: its part from S0, at most `rest`, must not overflow fp32.
-__device__ __forceinline__ Unit unit_of_r(float largest, float rest) { return unit_of<8>(fmaxf(largest, rest * 0x1p-60f)); }
+// The unit of R.  The next state is in it too: what is left of S0 in it, at most `rest`, must not overflow
+// fp32.  It exceeds R by 2^110 only where R does not count beside it, in the state as in the outputs.
+__device__ __forceinline__ Unit unit_of_r(float largest, float rest) { return unit_of<8>(fmaxf(largest, rest * 0x1p-110f)); }
 // A ratio of units, finite, so that what it multiplies stays zero if it is.
 __device__ __forceinline__ float finite(float ratio) { return fminf(ratio, 0x1p127f); }
 // The largest of the four lanes that have a column (lane, lane ^ 16, ^ 32, ^ 48).
@@ -763,11 +765,11 @@ __global__ __launch_bounds__(64 * kWalkWaves) void walk_kernel(GdnPrefillParams 
         const floatx4 bg = *reinterpret_cast<const floatx4*>(g1 + C + 16 * rt);
         U[rt] = be * conv_tile(rt) - bg * (X[rt] * xs);    // beta is 0 behind the chunk
       }
-      // from here on R, U, the state and, lifted, O are in the column's unit
+      // from here on R, U and the state are in the column's unit
       const float decay = g1[3 * C];
       Unit ru = {1.f, 1.f};
       if constexpr (NP == 1) ru = unit_of_r(column_max(largest(U)), decay * most * unit);
-      const float keep = NP == 1 ? decay * finite(unit * ru.inverse) : decay, ratio = NP == 1 ? finite(xs * ru.inverse) : 1.f;
+      const float keep = NP == 1 ? decay * finite(unit * ru.inverse) : decay;
       unit = NP == 1 ? ru.size : 1.f;
       // U = R + (T - I) R
       {
@@ -818,12 +820,13 @@ __global__ __launch_bounds__(64 * kWalkWaves) void walk_kernel(GdnPrefillParams 
         for (int rt = 0; rt < 4; ++rt) {
           const floatx4 eg = *reinterpret_cast<const floatx4*>(g2 + 16 * rt);
           const floatx4 qk = *reinterpret_cast<const floatx4*>(g2 + C + 16 * rt);
-          Y[rt] = eg * (Y[rt] * ratio) + qk * U[rt];
+          floatx4 Z = qk * U[rt];
 #pragma unroll
           for (int ks = 0; ks <= rt / 2; ++ks) {
             const Op<NP> a = get_op<NP>(Af, kTri, gdn_tri(rt, ks), lane);
-            Y[rt] = mul(a, uf[ks], Y[rt]);
+            Z = mul(a, uf[ks], Z);
           }
+          Y[rt] = eg * xs * Y[rt] + Z * (unit / kLift<NP>);
         }
       }
       pin(S);
@@ -836,7 +839,7 @@ __global__ __launch_bounds__(64 * kWalkWaves) void walk_kernel(GdnPrefillParams 
           const int i = 16 * rt + 4 * q4 + r;
           if (i < ce.len) {
             const int64_t at = ((int64_t)se.t0 + ce.tau0 + i) * p.o_stride + h * dv;
-            if (has) store_any(p.o, at + col, Y[rt][r] * (unit / kLift<NP>), NP == 1 ? 1 : p.o_bf16);
+            if (has) store_any(p.o, at + col, Y[rt][r], NP == 1 ? 1 : p.o_bf16);
           }
         }
       if (ce.ckpt_slot >= 0) put_slot(ce.ckpt_slot, ce.tau0 + ce.len);
@@ -884,7 +887,7 @@ template <int DK> struct Roles {
   static constexpr int B = 2 * C * DK + gdn_a_bytes(1);       // Q, Q K^T, gates: the output's
   static constexpr int V = 2 * C * 16 * 4;                    // v rows [ct][64/16][64 lanes][4], then U, lifted
   static constexpr int S = 2 * DK * 16 * 2;                   // S0 operands [ct][dk/32][64 lanes][8]
-  static constexpr int UN = 2 * 16 * 8;                       // [ct][16]: S0's unit in U's, and that of the lifted output
+  static constexpr int UN = 2 * 16 * 8;                       // [ct][16]: the units of S0 and of the lifted U
   // three places for v rows: the chain puts U where it found them, and the output reads that a step
   // later, while the rows after the next come in
   static constexpr int OFF_B = 2 * A, OFF_V = OFF_B + 2 * B, OFF_S = OFF_V + 3 * V, OFF_UN = OFF_S + 2 * S;
@@ -1041,14 +1044,14 @@ template <int DK> __device__ __forceinline__ void chain_role(const GdnPrefillPar
     floatx4 U[4];
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) U[rt] = be[rt] * v[rt] - bg[rt] * (X[rt] * xs);   // R; beta is 0 behind the chunk
-    // from here on R, U, the state and, lifted, O are in the column's unit
+    // from here on R, U and the state are in the column's unit
     const float decay = g1[3 * C];
     const Unit ru = unit_of_r(column_max(largest(U)), decay * most * unit);
     const float keep = decay * finite(unit * ru.inverse);
     unit = ru.size;
     if (q4 == 0)
       *reinterpret_cast<floatx2*>(u.smem + Ro::OFF_UN + now * Ro::UN + (u.wave * 16 + l16) * 8) =
-          floatx2{finite(xs * ru.inverse), unit / kLift<1>};
+          floatx2{xs, unit / kLift<1>};
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) U[rt] = U[rt] * ru.inverse;
     const Op<1> r0 = acc_op<1>(U[0], U[1]), r1 = acc_op<1>(U[2], U[3]);
@@ -1151,7 +1154,7 @@ template <int DK, int WHO> __device__ __forceinline__ void output_role(const Gdn
         }
       fence_order();
       store_out();
-      floatx4 Y[2][2];
+      floatx4 Y[2][2], Z[2][2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) Y[t][0] = Y[t][1] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -1161,7 +1164,7 @@ template <int DK, int WHO> __device__ __forceinline__ void output_role(const Gdn
 #pragma unroll
           for (int ct = 0; ct < 2; ++ct) Y[t][ct] = mfma(q[ks][t], s0[ks][ct], Y[t][ct]);
       floatx4 U[2][4], eg[2], qk[2];
-      floatx2 unit[2];   // S0's in U's, and that of the output
+      floatx2 unit[2];   // of S0 and of the lifted U
       Op<1> a[2], a1;
 #pragma unroll
       for (int ct = 0; ct < 2; ++ct)
@@ -1186,20 +1189,23 @@ template <int DK, int WHO> __device__ __forceinline__ void output_role(const Gdn
         const Op<1> u0 = acc_op<1>(U[ct][0] * lower, U[ct][1] * lower);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          Y[t][ct] = eg[t] * (Y[t][ct] * unit[ct][0]) + qk[t] * U[ct][RT[t]];
-          Y[t][ct] = mul(a[t], u0, Y[t][ct]);
+          Z[t][ct] = qk[t] * U[ct][RT[t]];
+          Z[t][ct] = mul(a[t], u0, Z[t][ct]);
         }
-        Y[1][ct] = mul(a1, acc_op<1>(U[ct][2] * lower, U[ct][3] * lower), Y[1][ct]);
+        Z[1][ct] = mul(a1, acc_op<1>(U[ct][2] * lower, U[ct][3] * lower), Z[1][ct]);
       }
-      pin(Y[0]);
-      pin(Y[1]);
+      pin(Z[0]);
+      pin(Z[1]);
       settle();
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
+        for (int ct = 0; ct < 2; ++ct) Y[t][ct] = eg[t] * unit[ct][0] * Y[t][ct] + Z[t][ct] * unit[ct][1];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
         for (int r = 0; r < 4; ++r)
-          out[t][r] = bits(from_f32<bf16>(Y[t][0][r] * unit[0][1])) |
-                      (uint32_t)bits(from_f32<bf16>(Y[t][1][r] * unit[1][1])) << 16;
+          out[t][r] = bits(from_f32<bf16>(Y[t][0][r])) | (uint32_t)bits(from_f32<bf16>(Y[t][1][r])) << 16;
       row = (int64_t)se.t0 + ce.tau0;
       len = ce.len;
     }

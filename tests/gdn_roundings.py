@@ -45,7 +45,7 @@ def prefill(shape, params, u, a, b, coarse=(), operand=fp16):
             su = unit(np.abs(S[h]).max(axis=0), 14)
             S0 = put("S", S[h] / su)
             R = be * (vc - np.exp(gc)[:, None] * (kc @ S0) * su)
-            ru = unit(np.maximum(np.abs(R).max(axis=0), 2.0 ** -60 * np.exp(gc[-1]) * np.abs(S[h]).max(axis=0)), 8)
+            ru = unit(np.maximum(np.abs(R).max(axis=0), 2.0 ** -110 * np.exp(gc[-1]) * np.abs(S[h]).max(axis=0)), 8)
             U = R / ru + Tm @ put("R", R / ru)
             o[r, h] = np.exp(gc)[:, None] * (qc @ S0) * su + ((q[r, h] * k[r, h]).sum(1)[:, None] * U + A @ put("U", U)) * ru
             S[h] = np.exp(gc[-1]) * S[h] + kc.T @ put("W", np.exp(gc[-1] - gc)[:, None] * U) * ru

@@ -395,3 +395,29 @@ def test_prefill_goes_on_from_a_wiped_state():
         for part in (slice(0, 64), slice(68, T)):
             assert rel(got[part].ravel(), ref[part].ravel(), 0) <= COLUMN_2NORM
         assert rel(host(L.pool.ssm[0, 1]).ravel(), L.ssm[1].ravel(), 0) <= COLUMN_2NORM
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 64, 32), (1, 1, 256, 32)], ids=str)
+def test_prefill_of_a_huge_state_that_nothing_is_written_to(shape):
+    """A state of 1e28 that two rows read with beta = 0, then wiped inside the chunk, then v of 1e-8 (a factor of 2^120):
+    the outputs of the first two rows are the state's, those of the rest v's, and all are finite."""
+    log(f"case: gdn prefill huge state, tiny rows {shape}")
+    Hk, Hv, dk, dv = shape
+    L = Layer(shape, 4, 3, 291, bias=False)
+    T = 70
+    L.params["conv_w"][2 * dk:] = [0, 0, 0, 1]
+    L.w.conv_w[2 * dk:] = torch.tensor([0.0, 0.0, 0.0, 1.0], device="cuda")
+    L.ssm[1], L.conv[1] = round_to(L.rng.normal(0, 1e28, L.ssm[1].shape), "bf16"), 0
+    L.pool.ssm[0, 1], L.pool.conv[0, 1] = torch.from_numpy(L.ssm[1]).to(torch.bfloat16).cuda(), 0
+    u, a, b = L.rows(T, "bf16")
+    u[:, 2 * dk:] = round_to(u[:, 2 * dk:] * 1e-8, "bf16")
+    b[:3], a[2] = -200.0, 3e4
+    o = L.out(T, "bf16")
+    L.pool.gdn_prefill(0, L.w, [0, T], [1], [1], *L.pool.split_qkv(dev(u, "bf16")), dev(a, "bf16"), dev(b, "bf16"), o)
+    torch.cuda.synchronize()
+    ref = orc.prefill(shape, L.ssm, L.conv, L.params, np.array([0, T]), [1], [1], None, u, a, b)
+    got = host(o)
+    assert np.isfinite(got).all()
+    for part in (slice(0, 2), slice(3, 64), slice(64, T)):
+        assert rel(got[part].ravel(), ref[part].ravel(), 0) <= COLUMN_2NORM, part
+    assert rel(host(L.pool.ssm[0, 1]).ravel(), L.ssm[1].ravel(), 0) <= COLUMN_2NORM
