@@ -414,7 +414,8 @@ m2_status mamba1_prefill(m2_pool* pool, int32_t layer, const m2_layer_params* pa
  *   S' = alpha S + beta (v - alpha S k^) k^T,   o = S' q^
  * Shapes of the three entry points below: dk in {32, 64, 128, 256}, dv a multiple
  * of 16, conv_kernel 2..4.
- * params: A [Hv] (negative, used as given), dt_bias [Hv], conv_w [d_conv][W]
+ * params: A [Hv] (negative, used as given: alpha <= 1, which the prefill's number
+ * ranges build on), dt_bias [Hv], conv_w [d_conv][W]
  * (16-byte aligned) and conv_b [d_conv] as in m2_layer_params, channels in the
  * order q (Hk*dk), k (Hk*dk), v (Hv*dv); conv_b may be NULL (no bias); D is not
  * read and may be NULL.
